@@ -71,6 +71,7 @@ typedef enum { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_PAIR 0x8u         /* copy pair names a block outside [0, num_blocks) */
 #define PA_DEVERR_WAIT_TIMEOUT 0x10u
 #define PA_DEVERR_CONFIG 0x20u      /* a kernel found less shared memory than it laid out; it did nothing */
+#define PA_DEVERR_POSITION 0x40u    /* pa_rope_append: a position outside [0, max_position) */
 
 /*
  * Shape of one paged KV cache and of the batch that reads it.
@@ -122,8 +123,20 @@ typedef struct {
  *                      q and out stay in shape->dtype.  The pages name FP8
  *                      only as a quantisation format that saves memory
  *                      (zingnex.cn sections 4.1 and 6; 5688vip.com section
- *                      2.3); this encoding is the library's reading. */
-typedef enum { PA_CACHE_AS_DTYPE = 0, PA_CACHE_FP8_E4M3 = 1 } pa_cache_format;
+ *                      2.3); this encoding is the library's reading.
+ *  PA_CACHE_FP4_E2M1   4-bit E2M1 codes (1 sign, 2 exponent bits, 1 mantissa
+ *                      bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), one E4M3 scale per 16
+ *                      consecutive dims of a head's row, and one fp32 scale per
+ *                      kv head for K and one for V: stored value = code * block
+ *                      scale * head scale.  4.5 bits an element.  A pool is
+ *                      bytes [num_blocks][num_kv_heads][block_size * head_dim *
+ *                      9 / 16]: a (block, head)'s run holds first the codes
+ *                      [block_size][head_dim / 2] (the even dim in a byte's low
+ *                      nibble), then the block scales [block_size][head_dim / 16].
+ *                      Written by pa_cache_append_fp4 and pa_rope_append, read
+ *                      by pa_decode_fp4 and pa_cache_gather; pa_copy_blocks and
+ *                      pa_swap_blocks move its blocks. */
+typedef enum { PA_CACHE_AS_DTYPE = 0, PA_CACHE_FP8_E4M3 = 1, PA_CACHE_FP4_E2M1 = 4 } pa_cache_format;
 
 /* How pa_decode computes QK^T and PV.  Both variants read K/V with tiled TMA
  * loads through the block table and keep the softmax in fp32.
@@ -219,7 +232,8 @@ size_t pa_decode_workspace_bytes(const pa_shape *shape, int32_t max_context_len)
  *   bytes, 16-byte aligned, never NULL.  It must not be shared with a decode
  *   that runs concurrently.
  * An E4M3 cache (cache_format PA_CACHE_FP8_E4M3) needs pa_decode_fp8 and its
- * scales: pa_decode refuses it with PA_ERR_INVALID_ARG.
+ * scales, an E2M1 cache pa_decode_fp4: pa_decode refuses both with
+ * PA_ERR_INVALID_ARG.
  * CUDA graphs: the call may be captured (stream capture) once the same shape
  * has run eagerly on that device, and the graph replayed any number of
  * times.  A captured call that uses the tensor-core kernels adds a memset
@@ -346,6 +360,88 @@ pa_status pa_decode_fp8(const void *q, const void *k_cache, const void *v_cache,
                         const int32_t *block_tables, const int32_t *context_lens, float scale,
                         void *out, const pa_shape *shape, int32_t max_context_len,
                         void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * Append into an E2M1 cache (shape->cache_format == PA_CACHE_FP4_E2M1, else
+ * PA_ERR_INVALID_ARG): as pa_cache_append, but a row of kv head h is stored
+ * per 16 consecutive dims x_0..x_15 as
+ *   s      = the E4M3 value nearest to (max|x_i| / 6) / k_scale[h], at most 448
+ *   code_i = the E2M1 code nearest to x_i * r,  r = 1 / (s * k_scale[h]), or 0
+ *            where s is 0
+ * every operation rounded once in fp32, nearest, ties to the even code,
+ * magnitudes of 6 and above saturated to 6 (and v likewise with v_scale).  A
+ * NaN among the dims makes s NaN, so that the 16 dims read back as NaN.  An
+ * infinity saturates s at 448.  k_scale, v_scale: device fp32 [num_kv_heads],
+ * finite and > 0 (not checked); max|x| / (6 * 448) of a head uses the block
+ * scales' range in full.
+ */
+pa_status pa_cache_append_fp4(const void *k, const void *v, const int32_t *slot_mapping,
+                              int32_t num_tokens, void *k_cache, void *v_cache,
+                              const float *k_scale, const float *v_scale,
+                              const pa_shape *shape, pa_stream_t stream);
+
+/*
+ * Decode attention over an E2M1 cache (shape->cache_format ==
+ * PA_CACHE_FP4_E2M1, else PA_ERR_INVALID_ARG): pa_decode's result with K_j and
+ * V_j the stored values.  Same workspace call as pa_decode.  Needs variant
+ * PA_DECODE_AUTO and no shared_prefix (else PA_ERR_UNSUPPORTED).  With
+ * partition_tokens 0 the partition follows from the batch and max_context_len
+ * (at most 2048): the workspace must have been sized with this call's
+ * max_context_len.
+ */
+pa_status pa_decode_fp4(const void *q, const void *k_cache, const void *v_cache,
+                        const float *k_scale, const float *v_scale,
+                        const int32_t *block_tables, const int32_t *context_lens, float scale,
+                        void *out, const pa_shape *shape, int32_t max_context_len,
+                        void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/* What pa_rope_append needs beside the shape.  Strides are elements between
+ * consecutive tokens, 0 for contiguous rows; multiples of 8, at least a token's
+ * row: q, k and v may be slices of one projection's output. */
+typedef struct {
+  int32_t rotary_dim;   /* leading dims of a head that rotate: a multiple of 16, <= head_dim */
+  int32_t interleaved;  /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1) */
+  int32_t max_position; /* rows of cos_sin */
+  int32_t reserved;     /* 0 */
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+} pa_rope;
+
+/*
+ * Append with the rotary position embedding applied on the way (any cache
+ * format): for t < num_tokens with slot_mapping[t] >= 0 and p = positions[t],
+ * every pair (a, b) of a head's rotated dims, number i of rotary_dim / 2, becomes
+ *   (a * c - b * s, b * c + a * s),  c = cos_sin[p][i], s = cos_sin[p][rotary_dim / 2 + i]
+ * in fp32 (each product and the sum rounded once), rounded to dtype; further
+ * dims are unchanged.  The rotated q[t] goes to q_out[t]; the rotated k[t] and
+ * v[t] go to slot slot_mapping[t] as pa_cache_append(_fp8, _fp4) would store
+ * them.  A token with a negative slot is padding: it is skipped, its q_out row
+ * left as it was.  A slot or position out of range is reported
+ * (PA_DEVERR_SLOT, PA_DEVERR_POSITION) and the token skipped.  Slots must be
+ * distinct; positions need not be.
+ * q, q_out [num_tokens][num_q_heads][head_dim]; k, v [num_tokens][num_kv_heads]
+ * [head_dim], with the strides of `rope`.  q_out may be q (with q's stride), else it
+ * must overlap no input.  positions: device int32 [num_tokens]; cos_sin: device
+ * fp32 [max_position][rotary_dim], 16-byte aligned.  k_scale, v_scale: device
+ * fp32 [num_kv_heads] for the quantised formats, NULL for PA_CACHE_AS_DTYPE.
+ */
+pa_status pa_rope_append(const void *q, const void *k, const void *v, const int32_t *positions,
+                         const float *cos_sin, const pa_rope *rope, const int32_t *slot_mapping,
+                         int32_t num_tokens, void *q_out, void *k_cache, void *v_cache,
+                         const float *k_scale, const float *v_scale, const pa_shape *shape,
+                         pa_stream_t stream);
+
+/*
+ * Cached rows back into contiguous rows of dtype (any cache format): row t of
+ * k_out and v_out, [num_tokens][num_kv_heads][head_dim], becomes the stored
+ * value of slot slot_mapping[t] (slots may repeat).  A 16-bit cache is copied bit
+ * by bit; code (* block scale) * head scale is formed in fp32 and rounded to
+ * dtype.  A negative slot leaves its row as it was; a slot beyond the pool
+ * reads as zeros and is reported (PA_DEVERR_SLOT).  k_scale, v_scale as in
+ * pa_rope_append (not read with PA_CACHE_AS_DTYPE).
+ */
+pa_status pa_cache_gather(const int32_t *slot_mapping, int32_t num_tokens, const void *k_cache,
+                          const void *v_cache, const float *k_scale, const float *v_scale,
+                          void *k_out, void *v_out, const pa_shape *shape, pa_stream_t stream);
 
 /*
  * Copy-on-write of whole blocks (zingnex.cn section 3.2 item 3): for each

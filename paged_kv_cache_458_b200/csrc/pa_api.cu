@@ -52,17 +52,22 @@ pa_status cuda_failed(const char* what) {
 void count_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Whether the tensor-core kernels run, with partition_tokens == 0 read as
 // "their default"; defined below.
 bool tensor_core_kernel(const pa_shape* s, int pt);
 int box_rows(const pa_shape* s);
 
+// The E2M1 decode splits finer where there is little work: see fp4_shape.
+constexpr int kFp4MaxPartition = 2048;
+
 // partition_tokens, or its default: 512 for the tensor-core kernels (their
 // largest item), 1024 for the CUDA-core kernel, where fewer partials measured
 // faster than 512 (llama2_7b 6025 vs 5697 GB/s, mistral_7b_gqa 4993 vs 4889).
 int effective_partition(const pa_shape* s) {
   if (s->partition_tokens != 0) return s->partition_tokens;
+  if (s->cache_format == PA_CACHE_FP4_E2M1) return kFp4MaxPartition;  // see fp4_shape
   return (s->shared_prefix || tensor_core_kernel(s, 512)) ? 512 : 1024;
 }
 
@@ -72,7 +77,8 @@ pa_status check_pool_shape(const pa_shape* s) {
   if (s->num_kv_heads <= 0 || s->head_dim <= 0 || s->block_size <= 0 || s->num_blocks < 0)
     return PA_ERR_INVALID_ARG;
   if (s->dtype != PA_F16 && s->dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
-  if (s->cache_format != PA_CACHE_AS_DTYPE && s->cache_format != PA_CACHE_FP8_E4M3)
+  if (s->cache_format != PA_CACHE_AS_DTYPE && s->cache_format != PA_CACHE_FP8_E4M3 &&
+      s->cache_format != PA_CACHE_FP4_E2M1)
     return PA_ERR_UNSUPPORTED;
   if (s->head_dim != 64 && s->head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (s->block_size % 8 != 0) return PA_ERR_UNSUPPORTED;
@@ -96,6 +102,13 @@ pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
       (s->head_dim != 128 || pt % pa::decode_tc_tile_tokens() != 0 || pt > 512))
     return PA_ERR_UNSUPPORTED;
   if (s->shared_prefix != 0 && s->shared_prefix != 1) return PA_ERR_INVALID_ARG;
+  if (s->cache_format == PA_CACHE_FP4_E2M1) {
+    if (s->variant != PA_DECODE_AUTO || s->shared_prefix) return PA_ERR_UNSUPPORTED;
+    const long long parts = ((long long)max_context_len + pt - 1) / pt;
+    // one CTA per (sequence, kv head, partition)
+    if ((parts > 0 ? parts : 1) * s->num_seqs > 0x7fffffffLL / s->num_kv_heads) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+  }
   if (s->shared_prefix &&
       (s->variant != PA_DECODE_AUTO || s->head_dim != 128 || pt % pa::decode_tc_tile_tokens() != 0 ||
        pt > 512))
@@ -107,9 +120,16 @@ pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
   return PA_OK;
 }
 
-// Whether pa_decode runs the tensor-core variant for this (valid) shape.
-// Bytes of one cached element.
+// Bytes of one cached element (16-bit and E4M3 caches).
 int cache_elem_bytes(const pa_shape* s) { return s->cache_format == PA_CACHE_FP8_E4M3 ? 1 : 2; }
+
+// Bytes of one block of one pool: with an E2M1 cache 9 bytes per 16 elements.
+long long cache_block_bytes(const pa_shape* s) {
+  const long long elems = (long long)s->block_size * s->num_kv_heads * s->head_dim;
+  return s->cache_format == PA_CACHE_FP4_E2M1 ? elems / 16 * 9 : elems * cache_elem_bytes(s);
+}
+
+// Whether pa_decode runs the tensor-core variant for this (valid) shape.
 
 bool tensor_core_kernel(const pa_shape* s, int pt) {
   if (s->variant == PA_DECODE_TENSOR_CORES) return true;
@@ -121,6 +141,19 @@ bool tensor_core_kernel(const pa_shape* s, int pt) {
   const int g = s->num_q_heads / s->num_kv_heads;
   return s->head_dim == 128 && (g >= 8 || (g >= 4 && box_rows(s) == 16)) &&
          pt % pa::decode_tc_tile_tokens() == 0 && pt <= 512;
+}
+
+// The shape that the E2M1 decode runs: its default partition is what gives the
+// batch about kFp4TargetItems items, in steps of 128 tokens.
+constexpr long long kFp4TargetItems = 1776;
+pa_shape fp4_shape(const pa_shape* s, int32_t max_context_len) {
+  pa_shape e = *s;
+  if (e.partition_tokens == 0) {
+    const long long tokens = (long long)max_context_len * s->num_seqs * s->num_kv_heads;
+    const long long want = (tokens / kFp4TargetItems + 127) / 128 * 128;
+    e.partition_tokens = (int)(want < 128 ? 128 : want > kFp4MaxPartition ? kFp4MaxPartition : want);
+  }
+  return e;
 }
 
 bool use_tensor_cores(const pa_shape* s) { return tensor_core_kernel(s, effective_partition(s)); }
@@ -284,6 +317,11 @@ extern "C" {
 
 size_t pa_decode_workspace_bytes(const pa_shape* shape, int32_t max_context_len) {
   if (check_decode_shape(shape, max_context_len) != PA_OK) return 0;
+  pa_shape resolved;
+  if (shape->cache_format == PA_CACHE_FP4_E2M1) {
+    resolved = fp4_shape(shape, max_context_len);
+    shape = &resolved;
+  }
   const long long head = kCounterBytes + plan_bytes(shape);
   const long long P = workspace_parts(shape, max_context_len);
   if (P == 0) return (size_t)head;
@@ -308,6 +346,7 @@ pa_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
   pa_status st = check_decode_shape(shape, max_context_len);
   if (st != PA_OK) return st;
   const bool fp8 = shape->cache_format == PA_CACHE_FP8_E4M3;
+  if (shape->cache_format == PA_CACHE_FP4_E2M1) return PA_ERR_INVALID_ARG;  // pa_decode_fp4
   if (fp8 != (k_scale != nullptr)) return PA_ERR_INVALID_ARG;  // the entry point must match
   if (shape->num_seqs == 0) return PA_OK;
   if (fp8 && (!v_scale || (reinterpret_cast<uintptr_t>(k_scale) & 3u) ||
@@ -568,6 +607,25 @@ bool multi_args_ok(const pa_shape* s, int num_query_tokens) {
          (long long)s->num_seqs * num_query_tokens <= (1LL << 30);
 }
 
+// Cache formats as pa_rope.cu numbers them.
+int kernel_format(const pa_shape* s) {
+  return s->cache_format == PA_CACHE_AS_DTYPE ? 0 : s->cache_format == PA_CACHE_FP8_E4M3 ? 1 : 2;
+}
+
+// The pool side of an append's arguments (pa_rope.cu), and the launch.
+pa_status append_rows(pa::RopeArgs& a, const pa_shape* s, int32_t num_tokens, pa_stream_t stream) {
+  a.num_kv_heads = s->num_kv_heads;
+  a.block_size = s->block_size;
+  a.num_slots = (long long)s->num_blocks * s->block_size;
+  a.err = error_word();
+  if (!a.err) return cuda_failed("device error word lookup failed");
+  int launched = 0;
+  cudaError_t e = pa::launch_rope_append(a, s->dtype, s->head_dim, kernel_format(s), num_tokens,
+                                         reinterpret_cast<cudaStream_t>(stream), &launched);
+  count_launches(launched);
+  return e == cudaSuccess ? PA_OK : cuda_failed(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -694,6 +752,180 @@ pa_status pa_cache_append_fp8(const void* k, const void* v, const int32_t* slot_
   return e == cudaSuccess ? PA_OK : cuda_failed(e);
 }
 
+pa_status pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                        const int32_t* context_lens, float scale, void* out, const pa_shape* shape,
+                        int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                        pa_stream_t stream) {
+  pa_status st = check_decode_shape(shape, max_context_len);
+  if (st != PA_OK) return st;
+  if (shape->cache_format != PA_CACHE_FP4_E2M1) return PA_ERR_INVALID_ARG;
+  if (shape->num_seqs == 0) return PA_OK;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !context_lens || !out)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_tables) || !aligned4(context_lens))
+    return PA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < pa_decode_workspace_bytes(shape, max_context_len))
+    return PA_ERR_INVALID_ARG;
+  if (max_context_len > (long long)shape->max_blocks_per_seq * shape->block_size)
+    return PA_ERR_INVALID_ARG;
+  if (shape->num_blocks == 0 && max_context_len > 0) return PA_ERR_INVALID_ARG;
+
+  const pa_shape e = fp4_shape(shape, max_context_len);
+  pa::DecodeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.out = static_cast<uint16_t*>(out);
+  a.num_parts = (int)workspace_parts(&e, max_context_len);
+  if (a.num_parts > 0) {
+    const long long rows = (long long)e.num_seqs * e.num_q_heads * a.num_parts;
+    char* ws = static_cast<char*>(workspace) + kCounterBytes;
+    a.ws_acc = reinterpret_cast<float*>(ws);
+    a.ws_ml = reinterpret_cast<float*>(ws + round256(rows * e.head_dim * 4));
+  } else {
+    a.num_parts = 1;
+  }
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.num_seqs = e.num_seqs;
+  a.num_q_heads = e.num_q_heads;
+  a.num_kv_heads = e.num_kv_heads;
+  a.group = e.num_q_heads / e.num_kv_heads;
+  a.block_size = e.block_size;
+  a.num_blocks = e.num_blocks;
+  a.max_blocks_per_seq = e.max_blocks_per_seq;
+  a.partition_tokens = a.own_tokens = e.partition_tokens;
+  a.grid_parts = a.num_parts;
+  a.query_tokens = 1;
+  a.max_context_len = max_context_len;
+  a.err = error_word();
+  if (!a.err) return cuda_failed("device error word lookup failed");
+  int launched = 0;
+  cudaError_t ce = pa::launch_decode_fp4(a, e.dtype, e.head_dim, a.group, k_cache, v_cache,
+                                         reinterpret_cast<cudaStream_t>(stream), &launched);
+  count_launches(launched);
+  return ce == cudaSuccess ? PA_OK : cuda_failed(ce);
+}
+
+pa_status pa_cache_append_fp4(const void* k, const void* v, const int32_t* slot_mapping,
+                              int32_t num_tokens, void* k_cache, void* v_cache,
+                              const float* k_scale, const float* v_scale, const pa_shape* shape,
+                              pa_stream_t stream) {
+  pa_status st = check_pool_shape(shape);
+  if (st != PA_OK) return st;
+  if (shape->cache_format != PA_CACHE_FP4_E2M1) return PA_ERR_INVALID_ARG;
+  if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!k || !v || !slot_mapping || !k_cache || !v_cache || !k_scale || !v_scale)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(slot_mapping) || !aligned4(k_scale) || !aligned4(v_scale))
+    return PA_ERR_INVALID_ARG;
+  pa::RopeArgs a{};  // no q rows, nothing rotated
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.slot_mapping = slot_mapping;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.k_stride = a.v_stride = (long long)shape->num_kv_heads * shape->head_dim;
+  return append_rows(a, shape, num_tokens, stream);
+}
+
+pa_status pa_rope_append(const void* q, const void* k, const void* v, const int32_t* positions,
+                         const float* cos_sin, const pa_rope* rope, const int32_t* slot_mapping,
+                         int32_t num_tokens, void* q_out, void* k_cache, void* v_cache,
+                         const float* k_scale, const float* v_scale, const pa_shape* shape,
+                         pa_stream_t stream) {
+  pa_status st = check_pool_shape(shape);
+  if (st != PA_OK) return st;
+  if (!rope || num_tokens < 0 || shape->num_q_heads <= 0 || rope->max_position <= 0 ||
+      (rope->interleaved != 0 && rope->interleaved != 1))
+    return PA_ERR_INVALID_ARG;
+  if (rope->rotary_dim <= 0 || rope->rotary_dim > shape->head_dim) return PA_ERR_INVALID_ARG;
+  if (rope->rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  // token strides in elements: 0 for contiguous rows, else no row may overlap the next
+  const long long q_row = (long long)shape->num_q_heads * shape->head_dim;
+  const long long kv_row = (long long)shape->num_kv_heads * shape->head_dim;
+  auto stride_ok = [](long long stride, long long row) { return stride == 0 || (stride >= row && stride % 8 == 0); };
+  if (!stride_ok(rope->q_stride, q_row) || !stride_ok(rope->q_out_stride, q_row) ||
+      !stride_ok(rope->k_stride, kv_row) || !stride_ok(rope->v_stride, kv_row))
+    return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!q || !k || !v || !positions || !cos_sin || !slot_mapping || !q_out || !k_cache || !v_cache)
+    return PA_ERR_INVALID_ARG;
+  // the scales belong to the quantised formats
+  const bool quantised = shape->cache_format != PA_CACHE_AS_DTYPE;
+  if (quantised != (k_scale != nullptr) || quantised != (v_scale != nullptr)) return PA_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, static_cast<const void*>(cos_sin), static_cast<const void*>(q_out),
+                        static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
+    if (!aligned16(p)) return PA_ERR_INVALID_ARG;
+  if (!aligned4(positions) || !aligned4(slot_mapping) || !aligned4(k_scale) || !aligned4(v_scale))
+    return PA_ERR_INVALID_ARG;
+  pa::RopeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.slot_mapping = slot_mapping;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.q_stride = rope->q_stride ? rope->q_stride : q_row;
+  a.q_out_stride = rope->q_out_stride ? rope->q_out_stride : q_row;
+  a.k_stride = rope->k_stride ? rope->k_stride : kv_row;
+  a.v_stride = rope->v_stride ? rope->v_stride : kv_row;
+  if (q_out == q && a.q_out_stride != a.q_stride) return PA_ERR_INVALID_ARG;  // in place: the same rows
+  a.num_q_heads = shape->num_q_heads;
+  a.rotary_dim = rope->rotary_dim;
+  a.interleaved = rope->interleaved;
+  a.max_position = rope->max_position;
+  return append_rows(a, shape, num_tokens, stream);
+}
+
+pa_status pa_cache_gather(const int32_t* slot_mapping, int32_t num_tokens, const void* k_cache,
+                          const void* v_cache, const float* k_scale, const float* v_scale,
+                          void* k_out, void* v_out, const pa_shape* shape, pa_stream_t stream) {
+  pa_status st = check_pool_shape(shape);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!slot_mapping || !k_cache || !v_cache || !k_out || !v_out) return PA_ERR_INVALID_ARG;
+  const bool quantised = shape->cache_format != PA_CACHE_AS_DTYPE;
+  if ((quantised && !(k_scale && v_scale)) || !aligned4(k_scale) || !aligned4(v_scale))
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) ||
+      !aligned4(slot_mapping))
+    return PA_ERR_INVALID_ARG;
+  pa::GatherArgs a{};
+  a.slot_mapping = slot_mapping;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.v_out = static_cast<uint16_t*>(v_out);
+  a.num_slots = (long long)shape->num_blocks * shape->block_size;
+  a.num_kv_heads = shape->num_kv_heads;
+  a.block_size = shape->block_size;
+  a.err = error_word();
+  if (!a.err) return cuda_failed("device error word lookup failed");
+  int launched = 0;
+  cudaError_t e = pa::launch_cache_gather(a, shape->dtype, shape->head_dim, kernel_format(shape), num_tokens,
+                                          reinterpret_cast<cudaStream_t>(stream), &launched);
+  count_launches(launched);
+  return e == cudaSuccess ? PA_OK : cuda_failed(e);
+}
+
 pa_status pa_copy_blocks(const int32_t* src_dst_pairs, int32_t num_pairs, void* k_cache,
                          void* v_cache, const pa_shape* shape, pa_stream_t stream) {
   pa_status st = check_pool_shape(shape);
@@ -704,8 +936,7 @@ pa_status pa_copy_blocks(const int32_t* src_dst_pairs, int32_t num_pairs, void* 
   if (!src_dst_pairs || !k_cache || !v_cache) return PA_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache) || (reinterpret_cast<uintptr_t>(src_dst_pairs) & 3u))
     return PA_ERR_INVALID_ARG;
-  const long long block_bytes = (long long)shape->block_size * shape->num_kv_heads *
-                                shape->head_dim * cache_elem_bytes(shape);
+  const long long block_bytes = cache_block_bytes(shape);
   unsigned int* err = error_word();
   if (!err) return cuda_failed("device error word lookup failed");
   int launched = 0;
@@ -730,8 +961,7 @@ pa_status pa_swap_blocks(const int32_t* src_dst_pairs, int32_t num_pairs, const 
       (reinterpret_cast<uintptr_t>(src_dst_pairs) & 3u))
     return PA_ERR_INVALID_ARG;
   // the pools must not overlap: a swap moves blocks between two pools
-  const long long block_bytes = (long long)shape->block_size * shape->num_kv_heads *
-                                shape->head_dim * cache_elem_bytes(shape);
+  const long long block_bytes = cache_block_bytes(shape);
   auto disjoint = [&](const void* a, long long na, const void* b, long long nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x + (uintptr_t)(na * block_bytes) <= y || y + (uintptr_t)(nb * block_bytes) <= x;
@@ -771,6 +1001,7 @@ int pa_decode_resolved_variant(const pa_shape* shape) {
   const pa_status st = check_decode_shape(shape, 0);
   if (st != PA_OK) return -(int)st;
   if (shape->shared_prefix) return PA_DECODE_RESOLVED_SHARED_PREFIX;
+  if (shape->cache_format == PA_CACHE_FP4_E2M1) return PA_DECODE_TENSOR_CORES;
   return use_tensor_cores(shape) ? PA_DECODE_TENSOR_CORES : PA_DECODE_CUDA_CORES;
 }
 

@@ -23,6 +23,7 @@ enum DeviceErrorBits : unsigned int {
   kErrPair = 1u << 3,         // a copy pair names a block outside the pool
   kErrWaitTimeout = 1u << 4,  // an mbarrier wait ran past its time limit
   kErrConfig = 1u << 5,       // a kernel could not lay out its shared memory (did nothing)
+  kErrPosition = 1u << 6,     // a token's position is outside the rotation table
 };
 
 // Kernels receive the address of the per-device error word (read and

@@ -1,0 +1,81 @@
+// pa_fp4.cuh -- the E2M1 (4-bit) cache: layout of its pools and conversions.
+//
+// A pool is [num_blocks][num_kv_heads] runs of block_size * D * 9 / 16 bytes:
+// first the codes [block_size][D / 2] (two E2M1 codes a byte, the even
+// dim in the low nibble), then the scales [block_size][D / 16] (one E4M3 code
+// per 16 dims).  Everything one (block, kv head) holds is one contiguous,
+// 16-byte aligned run, so a kernel that reads a head's tokens reads whole
+// lines, and a copy of a block is one copy.  The stored value of a dim is
+// code * block scale * head scale (the head scale one fp32 per kv head).
+#pragma once
+
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "pa_common.cuh"
+
+namespace pa {
+
+constexpr int kFp4Block = 16;  // dims that share a block scale
+
+// Bytes of one (block, kv head) run, and of its codes.
+__host__ __device__ constexpr long long fp4_head_bytes(int block_size, int head_dim) {
+  return (long long)block_size * head_dim * 9 / 16;
+}
+__host__ __device__ constexpr long long fp4_code_bytes(int block_size, int head_dim) {
+  return (long long)block_size * head_dim / 2;
+}
+
+// Eight E2M1 codes (low nibble first) -> eight f16 values, exact.  For words
+// loaded whole: unpacking a zero-extended byte this way gave zeros (nvcc 12.9);
+// e2m1x2_to_f2 takes single bytes.
+__device__ __forceinline__ void e2m1x8_to_h2(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+
+// Two E2M1 codes (low nibble first) -> two floats, exact.
+__device__ __forceinline__ float2 e2m1x2_to_f2(uint8_t b) {
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(b), __NV_E2M1);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Two E4M3 codes (low byte first) -> f16x2, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint16_t u) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+__device__ __forceinline__ float e4m3_to_f(uint8_t u) { return e4m3x2_to_f2((uint16_t)u).x; }
+
+__device__ __forceinline__ float2 h2_to_f2(uint32_t u) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// The block scale of 16 dims whose largest magnitude is `amax` under head
+// scale `hs`: the E4M3 value nearest to (amax / 6) / hs, 6 being E2M1's
+// largest, saturating at 448; NaN where a dim is NaN.  *r is the factor
+// that takes a value to the code's range, 1 / (scale * hs), or 0 for a zero scale.
+__device__ __forceinline__ uint8_t fp4_block_scale(float amax, bool nan, float hs, float* r) {
+  const float want = __fdiv_rn(__fdiv_rn(amax, 6.f), hs);
+  const uint8_t s = nan ? 0x7f : (uint8_t)__nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
+  const float f = e4m3_to_f(s);
+  *r = f > 0.f ? __fdiv_rn(1.f, __fmul_rn(f, hs)) : 0.f;
+  return s;
+}
+
+// Two values -> two E2M1 codes in a byte (x in the low nibble): nearest, ties
+// to the even code, saturating at 6.
+__device__ __forceinline__ uint32_t e2m1x2_of(float x, float y) {
+  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x, y), __NV_E2M1, cudaRoundNearest);
+}
+
+}  // namespace pa

@@ -133,4 +133,48 @@ cudaError_t launch_copy_blocks(const int32_t* pairs, int num_pairs, const void* 
                                int dst_blocks, long long block_bytes, unsigned int* err,
                                cudaStream_t stream, int* launches);
 
+// The rotating append (pa_rope.cu): num_q_heads 0 leaves q out, rotary_dim 0
+// rotates nothing.  Strides are in elements between tokens.
+struct RopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  const int32_t* positions;
+  const float* cos_sin;          // [max_position][rotary_dim]: cos, then sin
+  const int32_t* slot_mapping;
+  uint16_t* q_out;
+  void* k_cache;
+  void* v_cache;
+  const float* k_scale;          // [Hkv] with a quantised cache
+  const float* v_scale;
+  unsigned int* err;
+  long long q_stride, k_stride, v_stride, q_out_stride, num_slots;
+  int num_q_heads, num_kv_heads, block_size;
+  int rotary_dim, interleaved, max_position;
+};
+// format: 0 the element type, 1 E4M3, 2 E2M1.
+cudaError_t launch_rope_append(const RopeArgs& a, int dtype, int head_dim, int format, int num_tokens,
+                               cudaStream_t stream, int* launches);
+
+// Cached rows back into 16-bit rows (pa_rope.cu).
+struct GatherArgs {
+  const int32_t* slot_mapping;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  uint16_t* k_out;
+  uint16_t* v_out;
+  unsigned int* err;
+  long long num_slots;
+  int num_kv_heads, block_size;
+};
+cudaError_t launch_cache_gather(const GatherArgs& a, int dtype, int head_dim, int format, int num_tokens,
+                                cudaStream_t stream, int* launches);
+
+// Attention over an E2M1 cache (pa_decode_fp4.cu): the partition kernel, then
+// the merge where contexts span several partitions.
+cudaError_t launch_decode_fp4(const DecodeArgs& a, int dtype, int head_dim, int group, const void* k_pool,
+                              const void* v_pool, cudaStream_t stream, int* launches);
+
 }  // namespace pa

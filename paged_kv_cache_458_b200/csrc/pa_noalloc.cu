@@ -49,7 +49,7 @@ extern "C" pa_status pa_decode_noalloc(const void* q, const void* k_cache, const
                                        const int32_t* block_tables, const int32_t* context_lens,
                                        float scale, void* out, const pa_shape* shape,
                                        int32_t max_context_len, pa_stream_t stream) {
-  if (!shape) return PA_ERR_INVALID_ARG;
+  if (!shape || shape->cache_format == PA_CACHE_FP4_E2M1) return PA_ERR_INVALID_ARG;
   const size_t need = pa_decode_workspace_bytes(shape, max_context_len);
   if (need > (size_t)PA_NOALLOC_SCRATCH_BYTES) return PA_ERR_UNSUPPORTED;
   void* scratch = nullptr;

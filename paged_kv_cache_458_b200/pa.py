@@ -21,12 +21,14 @@ PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_OOM, PA_ERR_D
 PA_F16, PA_BF16 = 0, 1
 PA_DECODE_AUTO, PA_DECODE_CUDA_CORES, PA_DECODE_TENSOR_CORES = 0, 1, 2
 PA_DECODE_RESOLVED_SHARED_PREFIX = 3
-PA_CACHE_AS_DTYPE, PA_CACHE_FP8_E4M3 = 0, 1
+PA_CACHE_AS_DTYPE, PA_CACHE_FP8_E4M3, PA_CACHE_FP4_E2M1 = 0, 1, 4
 PA_DEVERR_BLOCK_ID = 0x1
 PA_DEVERR_CONTEXT_LEN = 0x2
 PA_DEVERR_SLOT = 0x4
 PA_DEVERR_PAIR = 0x8
 PA_DEVERR_WAIT_TIMEOUT = 0x10
+PA_DEVERR_CONFIG = 0x20
+PA_DEVERR_POSITION = 0x40
 
 
 class LibraryMissing(ImportError):
@@ -52,6 +54,11 @@ class pa_shape(ctypes.Structure):
         return "pa_shape(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class pa_rope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rotary_dim", "interleaved", "max_position", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -72,6 +79,14 @@ def _declare(lib):
     lib.pa_cache_append_fp8.argtypes = [P, P, P, I32, P, P, P, P, SP, P]
     lib.pa_decode_fp8.restype = c.c_int
     lib.pa_decode_fp8.argtypes = [P, P, P, P, P, P, P, c.c_float, P, SP, I32, P, SZ, P]
+    lib.pa_cache_append_fp4.restype = c.c_int
+    lib.pa_cache_append_fp4.argtypes = [P, P, P, I32, P, P, P, P, SP, P]
+    lib.pa_decode_fp4.restype = c.c_int
+    lib.pa_decode_fp4.argtypes = [P, P, P, P, P, P, P, c.c_float, P, SP, I32, P, SZ, P]
+    lib.pa_rope_append.restype = c.c_int
+    lib.pa_rope_append.argtypes = [P, P, P, P, P, c.POINTER(pa_rope), P, I32, P, P, P, P, P, SP, P]
+    lib.pa_cache_gather.restype = c.c_int
+    lib.pa_cache_gather.argtypes = [P, I32, P, P, P, P, P, P, SP, P]
     lib.pa_copy_blocks.restype = c.c_int
     lib.pa_copy_blocks.argtypes = [P, I32, P, P, SP, P]
     lib.pa_swap_blocks.restype = c.c_int
@@ -253,6 +268,49 @@ def pa_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_l
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
         _ptr(context_lens), float(scale), _ptr(out), ctypes.byref(shape), int(max_context_len),
         _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def pa_cache_append_fp4(k, v, slot_mapping, num_tokens: int, k_cache, v_cache, k_scale, v_scale,
+                        shape: pa_shape, stream=None) -> None:
+    """Append into an E2M1 cache (see pa.h)."""
+    _check("pa_cache_append_fp4", lib().pa_cache_append_fp4(
+        _ptr(k), _ptr(v), _ptr(slot_mapping), int(num_tokens), _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), ctypes.byref(shape), _stream(stream)))
+
+
+def pa_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale: float,
+                  out, shape: pa_shape, max_context_len: int, workspace=None,
+                  workspace_bytes: int | None = None, stream=None) -> None:
+    """Decode attention over an E2M1 cache (see pa.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("pa_decode_fp4", lib().pa_decode_fp4(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+        _ptr(context_lens), float(scale), _ptr(out), ctypes.byref(shape), int(max_context_len),
+        _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def make_rope(*, rotary_dim, max_position, interleaved=0, q_stride=0, k_stride=0, v_stride=0,
+              q_out_stride=0) -> pa_rope:
+    """Rotation parameters of pa_rope_append; strides in elements between tokens, 0 = contiguous."""
+    return pa_rope(rotary_dim, interleaved, max_position, 0, q_stride, k_stride, v_stride, q_out_stride)
+
+
+def pa_rope_append(q, k, v, positions, cos_sin, rope: pa_rope, slot_mapping, num_tokens: int, q_out,
+                   k_cache, v_cache, k_scale, v_scale, shape: pa_shape, stream=None) -> None:
+    """Append with the rotary position embedding applied on the way (see pa.h)."""
+    _check("pa_rope_append", lib().pa_rope_append(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(cos_sin), ctypes.byref(rope), _ptr(slot_mapping),
+        int(num_tokens), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        ctypes.byref(shape), _stream(stream)))
+
+
+def pa_cache_gather(slot_mapping, num_tokens: int, k_cache, v_cache, k_scale, v_scale, k_out, v_out,
+                    shape: pa_shape, stream=None) -> None:
+    """Cached rows back into contiguous 16-bit rows (see pa.h)."""
+    _check("pa_cache_gather", lib().pa_cache_gather(
+        _ptr(slot_mapping), int(num_tokens), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(k_out), _ptr(v_out), ctypes.byref(shape), _stream(stream)))
 
 
 def pa_copy_blocks(src_dst_pairs, num_pairs: int, k_cache, v_cache, shape: pa_shape,
