@@ -134,6 +134,8 @@ def _declare(lib):
 def lib():
     """The loaded libpa.so (raises LibraryMissing if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -172,11 +174,20 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
-def _stream(stream) -> int | None:
-    if stream is None:
-        import torch
+_current_stream = None
 
-        return torch.cuda.current_stream().cuda_stream
+
+def _stream(stream) -> int | None:
+    global _current_stream
+    if stream is None:
+        if _current_stream is None:
+            import torch
+
+            torch.cuda.current_stream()  # initialises CUDA
+            # the handle without a Stream object around it: 0.2 us instead of 3.2 us a call
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _current_stream = lambda: raw(device())  # noqa: E731
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
