@@ -59,15 +59,12 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool tensor_core_kernel(const pa_shape* s, int pt);
 int box_rows(const pa_shape* s);
 
-// The E2M1 decode splits finer where there is little work: see fp4_shape.
-constexpr int kFp4MaxPartition = 2048;
-
 // partition_tokens, or its default: 512 for the tensor-core kernels (their
 // largest item), 1024 for the CUDA-core kernel, where fewer partials measured
 // faster than 512 (llama2_7b 6025 vs 5697 GB/s, mistral_7b_gqa 4993 vs 4889).
 int effective_partition(const pa_shape* s) {
   if (s->partition_tokens != 0) return s->partition_tokens;
-  if (s->cache_format == PA_CACHE_FP4_E2M1) return kFp4MaxPartition;  // see fp4_shape
+  if (s->cache_format == PA_CACHE_FP4_E2M1) return 128;  // the least a CTA takes
   return (s->shared_prefix || tensor_core_kernel(s, 512)) ? 512 : 1024;
 }
 
@@ -84,6 +81,14 @@ pa_status check_pool_shape(const pa_shape* s) {
   if (s->block_size % 8 != 0) return PA_ERR_UNSUPPORTED;
   if ((long long)s->num_blocks * s->block_size >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
   return PA_OK;
+}
+
+// CTAs of the E2M1 decode; 0 where the batch may hold too many chunks of 32 tokens.
+int fp4_ctas(const pa_shape* s, int32_t max_context_len) {
+  if (s->num_seqs == 0) return 1;
+  if (s->num_seqs > 0x7fffffff / s->num_q_heads) return 0;
+  return pa::fp4_decode_ctas(s->num_seqs, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, max_context_len,
+                             s->partition_tokens);
 }
 
 pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
@@ -104,10 +109,7 @@ pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
   if (s->shared_prefix != 0 && s->shared_prefix != 1) return PA_ERR_INVALID_ARG;
   if (s->cache_format == PA_CACHE_FP4_E2M1) {
     if (s->variant != PA_DECODE_AUTO || s->shared_prefix) return PA_ERR_UNSUPPORTED;
-    const long long parts = ((long long)max_context_len + pt - 1) / pt;
-    // one CTA per (sequence, kv head, partition)
-    if ((parts > 0 ? parts : 1) * s->num_seqs > 0x7fffffffLL / s->num_kv_heads) return PA_ERR_UNSUPPORTED;
-    return PA_OK;
+    return fp4_ctas(s, max_context_len) > 0 ? PA_OK : PA_ERR_UNSUPPORTED;
   }
   if (s->shared_prefix &&
       (s->variant != PA_DECODE_AUTO || s->head_dim != 128 || pt % pa::decode_tc_tile_tokens() != 0 ||
@@ -141,19 +143,6 @@ bool tensor_core_kernel(const pa_shape* s, int pt) {
   const int g = s->num_q_heads / s->num_kv_heads;
   return s->head_dim == 128 && (g >= 8 || (g >= 4 && box_rows(s) == 16)) &&
          pt % pa::decode_tc_tile_tokens() == 0 && pt <= 512;
-}
-
-// The shape that the E2M1 decode runs: its default partition is what gives the
-// batch about kFp4TargetItems items, in steps of 128 tokens.
-constexpr long long kFp4TargetItems = 1776;
-pa_shape fp4_shape(const pa_shape* s, int32_t max_context_len) {
-  pa_shape e = *s;
-  if (e.partition_tokens == 0) {
-    const long long tokens = (long long)max_context_len * s->num_seqs * s->num_kv_heads;
-    const long long want = (tokens / kFp4TargetItems + 127) / 128 * 128;
-    e.partition_tokens = (int)(want < 128 ? 128 : want > kFp4MaxPartition ? kFp4MaxPartition : want);
-  }
-  return e;
 }
 
 bool use_tensor_cores(const pa_shape* s) { return tensor_core_kernel(s, effective_partition(s)); }
@@ -207,6 +196,22 @@ long long workspace_parts(const pa_shape* s, int32_t max_context_len) {
   const long long P = num_partitions(s, max_context_len);
   if (s->shared_prefix) return P + 2;
   return P > 1 ? P : 0;
+}
+
+// Workspace of the E2M1 decode, in bytes: per CTA two partials of `group` rows
+// in fp32, their (max, sum) pairs, and the spans of every (sequence, kv head).
+struct Fp4Workspace {
+  int ctas;
+  long long ml, parts, bytes;  // offsets; the rows are at 0
+};
+Fp4Workspace fp4_workspace(const pa_shape* s, int32_t max_context_len) {
+  Fp4Workspace w;
+  w.ctas = fp4_ctas(s, max_context_len);
+  const long long rows = 2LL * w.ctas * (s->num_q_heads / s->num_kv_heads);
+  w.ml = round256(rows * s->head_dim * 4);
+  w.parts = w.ml + round256(rows * 8);
+  w.bytes = w.parts + round256(8LL * s->num_seqs * s->num_kv_heads) + 256;
+  return w;
 }
 
 // Tags of decode launches (see the work counter in pa_decode_tc.cu): unique
@@ -317,10 +322,9 @@ extern "C" {
 
 size_t pa_decode_workspace_bytes(const pa_shape* shape, int32_t max_context_len) {
   if (check_decode_shape(shape, max_context_len) != PA_OK) return 0;
-  pa_shape resolved;
   if (shape->cache_format == PA_CACHE_FP4_E2M1) {
-    resolved = fp4_shape(shape, max_context_len);
-    shape = &resolved;
+    const Fp4Workspace w = fp4_workspace(shape, max_context_len);
+    return (size_t)w.bytes;
   }
   const long long head = kCounterBytes + plan_bytes(shape);
   const long long P = workspace_parts(shape, max_context_len);
@@ -774,39 +778,32 @@ pa_status pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
     return PA_ERR_INVALID_ARG;
   if (shape->num_blocks == 0 && max_context_len > 0) return PA_ERR_INVALID_ARG;
 
-  const pa_shape e = fp4_shape(shape, max_context_len);
+  const Fp4Workspace w = fp4_workspace(shape, max_context_len);
+  char* ws = static_cast<char*>(workspace);
   pa::DecodeArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.block_tables = block_tables;
   a.context_lens = context_lens;
   a.out = static_cast<uint16_t*>(out);
-  a.num_parts = (int)workspace_parts(&e, max_context_len);
-  if (a.num_parts > 0) {
-    const long long rows = (long long)e.num_seqs * e.num_q_heads * a.num_parts;
-    char* ws = static_cast<char*>(workspace) + kCounterBytes;
-    a.ws_acc = reinterpret_cast<float*>(ws);
-    a.ws_ml = reinterpret_cast<float*>(ws + round256(rows * e.head_dim * 4));
-  } else {
-    a.num_parts = 1;
-  }
+  a.ws_acc = reinterpret_cast<float*>(ws);
+  a.ws_ml = reinterpret_cast<float*>(ws + w.ml);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.num_seqs = e.num_seqs;
-  a.num_q_heads = e.num_q_heads;
-  a.num_kv_heads = e.num_kv_heads;
-  a.group = e.num_q_heads / e.num_kv_heads;
-  a.block_size = e.block_size;
-  a.num_blocks = e.num_blocks;
-  a.max_blocks_per_seq = e.max_blocks_per_seq;
-  a.partition_tokens = a.own_tokens = e.partition_tokens;
-  a.grid_parts = a.num_parts;
-  a.query_tokens = 1;
+  a.num_seqs = shape->num_seqs;
+  a.num_q_heads = shape->num_q_heads;
+  a.num_kv_heads = shape->num_kv_heads;
+  a.group = shape->num_q_heads / shape->num_kv_heads;
+  a.block_size = shape->block_size;
+  a.num_blocks = shape->num_blocks;
+  a.max_blocks_per_seq = shape->max_blocks_per_seq;
+  a.grid_parts = w.ctas;
   a.max_context_len = max_context_len;
   a.err = error_word();
   if (!a.err) return cuda_failed("device error word lookup failed");
   int launched = 0;
-  cudaError_t ce = pa::launch_decode_fp4(a, e.dtype, e.head_dim, a.group, k_cache, v_cache,
+  cudaError_t ce = pa::launch_decode_fp4(a, shape->dtype, shape->head_dim, k_cache, v_cache,
+                                         reinterpret_cast<int2*>(ws + w.parts),
                                          reinterpret_cast<cudaStream_t>(stream), &launched);
   count_launches(launched);
   return ce == cudaSuccess ? PA_OK : cuda_failed(ce);

@@ -172,9 +172,12 @@ struct GatherArgs {
 cudaError_t launch_cache_gather(const GatherArgs& a, int dtype, int head_dim, int format, int num_tokens,
                                 cudaStream_t stream, int* launches);
 
-// Attention over an E2M1 cache (pa_decode_fp4.cu): the partition kernel, then
-// the merge where contexts span several partitions.
-cudaError_t launch_decode_fp4(const DecodeArgs& a, int dtype, int head_dim, int group, const void* k_pool,
-                              const void* v_pool, cudaStream_t stream, int* launches);
+// Attention over an E2M1 cache (pa_decode_fp4.cu).  a.grid_parts CTAs (from
+// fp4_decode_ctas; 0: too many chunks) split the batch; a.ws_acc, a.ws_ml
+// hold 2 * CTAs * group partial rows, item_parts [num_seqs][Hkv] the spans an
+// item lies in.
+int fp4_decode_ctas(int num_seqs, int num_kv_heads, int group, int max_context_len, int partition_tokens);
+cudaError_t launch_decode_fp4(const DecodeArgs& a, int dtype, int head_dim, const void* k_pool, const void* v_pool,
+                              int2* item_parts, cudaStream_t stream, int* launches);
 
 }  // namespace pa
