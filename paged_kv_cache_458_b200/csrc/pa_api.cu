@@ -64,7 +64,7 @@ int box_rows(const pa_shape* s);
 // faster than 512 (llama2_7b 6025 vs 5697 GB/s, mistral_7b_gqa 4993 vs 4889).
 int effective_partition(const pa_shape* s) {
   if (s->partition_tokens != 0) return s->partition_tokens;
-  if (s->cache_format == PA_CACHE_FP4_E2M1) return 128;  // the least a CTA takes
+  if (s->cache_format == PA_CACHE_FP4_E2M1) return 64;  // the least a warp takes
   return (s->shared_prefix || tensor_core_kernel(s, 512)) ? 512 : 1024;
 }
 
@@ -81,14 +81,6 @@ pa_status check_pool_shape(const pa_shape* s) {
   if (s->block_size % 8 != 0) return PA_ERR_UNSUPPORTED;
   if ((long long)s->num_blocks * s->block_size >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
   return PA_OK;
-}
-
-// CTAs of the E2M1 decode; 0 where the batch may hold too many chunks of 32 tokens.
-int fp4_ctas(const pa_shape* s, int32_t max_context_len) {
-  if (s->num_seqs == 0) return 1;
-  if (s->num_seqs > 0x7fffffff / s->num_q_heads) return 0;
-  return pa::fp4_decode_ctas(s->num_seqs, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, max_context_len,
-                             s->partition_tokens);
 }
 
 pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
@@ -109,7 +101,10 @@ pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
   if (s->shared_prefix != 0 && s->shared_prefix != 1) return PA_ERR_INVALID_ARG;
   if (s->cache_format == PA_CACHE_FP4_E2M1) {
     if (s->variant != PA_DECODE_AUTO || s->shared_prefix) return PA_ERR_UNSUPPORTED;
-    return fp4_ctas(s, max_context_len) > 0 ? PA_OK : PA_ERR_UNSUPPORTED;
+    pa::Fp4Split split;
+    if (s->num_seqs > 0x7fffffff / s->num_q_heads) return PA_ERR_UNSUPPORTED;
+    return pa::fp4_decode_split(s->num_seqs, s->num_kv_heads, max_context_len, s->partition_tokens, &split)
+               ? PA_OK : PA_ERR_UNSUPPORTED;
   }
   if (s->shared_prefix &&
       (s->variant != PA_DECODE_AUTO || s->head_dim != 128 || pt % pa::decode_tc_tile_tokens() != 0 ||
@@ -198,16 +193,16 @@ long long workspace_parts(const pa_shape* s, int32_t max_context_len) {
   return P > 1 ? P : 0;
 }
 
-// Workspace of the E2M1 decode, in bytes: per CTA two partials of `group` rows
+// Workspace of the E2M1 decode, in bytes: per worker two partials of `group` rows
 // in fp32, their (max, sum) pairs, and the spans of every (sequence, kv head).
 struct Fp4Workspace {
-  int ctas;
+  pa::Fp4Split split;
   long long ml, parts, bytes;  // offsets; the rows are at 0
 };
 Fp4Workspace fp4_workspace(const pa_shape* s, int32_t max_context_len) {
   Fp4Workspace w;
-  w.ctas = fp4_ctas(s, max_context_len);
-  const long long rows = 2LL * w.ctas * (s->num_q_heads / s->num_kv_heads);
+  pa::fp4_decode_split(s->num_seqs, s->num_kv_heads, max_context_len, s->partition_tokens, &w.split);
+  const long long rows = 2LL * w.split.workers * (s->num_q_heads / s->num_kv_heads);
   w.ml = round256(rows * s->head_dim * 4);
   w.parts = w.ml + round256(rows * 8);
   w.bytes = w.parts + round256(8LL * s->num_seqs * s->num_kv_heads) + 256;
@@ -797,12 +792,11 @@ pa_status pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
   a.block_size = shape->block_size;
   a.num_blocks = shape->num_blocks;
   a.max_blocks_per_seq = shape->max_blocks_per_seq;
-  a.grid_parts = w.ctas;
   a.max_context_len = max_context_len;
   a.err = error_word();
   if (!a.err) return cuda_failed("device error word lookup failed");
   int launched = 0;
-  cudaError_t ce = pa::launch_decode_fp4(a, shape->dtype, shape->head_dim, k_cache, v_cache,
+  cudaError_t ce = pa::launch_decode_fp4(a, shape->dtype, shape->head_dim, k_cache, v_cache, w.split,
                                          reinterpret_cast<int2*>(ws + w.parts),
                                          reinterpret_cast<cudaStream_t>(stream), &launched);
   count_launches(launched);

@@ -172,12 +172,14 @@ struct GatherArgs {
 cudaError_t launch_cache_gather(const GatherArgs& a, int dtype, int head_dim, int format, int num_tokens,
                                 cudaStream_t stream, int* launches);
 
-// Attention over an E2M1 cache (pa_decode_fp4.cu).  a.grid_parts CTAs (from
-// fp4_decode_ctas; 0: too many chunks) split the batch; a.ws_acc, a.ws_ml
-// hold 2 * CTAs * group partial rows, item_parts [num_seqs][Hkv] the spans an
-// item lies in.
-int fp4_decode_ctas(int num_seqs, int num_kv_heads, int group, int max_context_len, int partition_tokens);
+// Attention over an E2M1 cache (pa_decode_fp4.cu): how a batch is split (false:
+// too many chunks).  a.ws_acc, a.ws_ml hold 2 * workers * group partial rows,
+// item_parts [num_seqs][Hkv] the workers an item is split over.
+struct Fp4Split {
+  int ctas, workers, team;  // team: warps per worker
+};
+bool fp4_decode_split(int num_seqs, int num_kv_heads, int max_context_len, int partition_tokens, Fp4Split* split);
 cudaError_t launch_decode_fp4(const DecodeArgs& a, int dtype, int head_dim, const void* k_pool, const void* v_pool,
-                              int2* item_parts, cudaStream_t stream, int* launches);
+                              const Fp4Split& split, int2* item_parts, cudaStream_t stream, int* launches);
 
 }  // namespace pa
