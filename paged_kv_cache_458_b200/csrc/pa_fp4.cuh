@@ -60,16 +60,10 @@ __device__ __forceinline__ float2 h2_to_f2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
-// The block scale of 16 dims whose largest magnitude is `amax` under head
-// scale `hs`: the E4M3 value nearest to (amax / 6) / hs, 6 being E2M1's
-// largest, saturating at 448; NaN where a dim is NaN.  *r is the factor
-// that takes a value to the code's range, 1 / (scale * hs), or 0 for a zero scale.
-__device__ __forceinline__ uint8_t fp4_block_scale(float amax, bool nan, float hs, float* r) {
-  const float want = __fdiv_rn(__fdiv_rn(amax, 6.f), hs);
-  const uint8_t s = nan ? 0x7f : (uint8_t)__nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
-  const float f = e4m3_to_f(s);
-  *r = f > 0.f ? __fdiv_rn(1.f, __fmul_rn(f, hs)) : 0.f;
-  return s;
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Two values -> two E2M1 codes in a byte (x in the low nibble): nearest, ties
