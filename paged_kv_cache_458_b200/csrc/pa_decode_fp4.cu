@@ -104,13 +104,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Untiled bulk copy global -> shared, completion counted on an mbarrier; addresses and size in 16 bytes.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 // GT: the group's query heads, at most: 4, 8 or 16.  R: tokens of one copy.
 template <typename T, int D, int GT, int R>
 __global__ void __launch_bounds__(kFp4Warps * 32, kFp4Ctas)
@@ -757,15 +750,9 @@ cudaError_t launch_fp4(const DecodeArgs& a, const void* k, const void* v, const 
                        cudaStream_t stream, int* launches) {
   using L = Fp4Smem<D, GT>;
   auto* kern = decode_fp4_kernel<T, D, GT, R>;
-  static std::atomic<uint64_t> configured{0};  // a bit per device; setting the attribute twice is harmless
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = allow_smem(kern, L::kTotalMerge, &configured);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(configured.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotalMerge);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
   e = launch_pdl(kern, dim3(w.ctas), dim3(kFp4Warps * 32), w.team == 1 ? L::kTotal : L::kTotalMerge, stream, a,
                  static_cast<const unsigned char*>(k), static_cast<const unsigned char*>(v), w.workers, w.team, parts);
   if (e == cudaSuccess) ++*launches;

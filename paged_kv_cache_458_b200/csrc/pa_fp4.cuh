@@ -66,10 +66,4 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Two values -> two E2M1 codes in a byte (x in the low nibble): nearest, ties
-// to the even code, saturating at 6.
-__device__ __forceinline__ uint32_t e2m1x2_of(float x, float y) {
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x, y), __NV_E2M1, cudaRoundNearest);
-}
-
 }  // namespace pa

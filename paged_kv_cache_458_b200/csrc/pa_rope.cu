@@ -7,14 +7,18 @@
 // is rounded once to the element type, before any quantisation: a cache of any
 // format is built from the same rotated rows.
 //
-// Work split: a head's row of D elements is D / 8 units of 16 bytes, one lane
-// each, so that a warp holds 2 (D 128) or 4 (D 64) whole rows: the partner unit
-// of the half pairing comes by shuffle, and a row may be rotated in place.  A
-// warp walks over tokens with a fixed slice of the token's rows: where a row comes from and
-// goes to, its head's scale and the scale's reciprocal are worked out once, and per token
-// only the slot's and the position's offsets are left.  An append has the next
-// token's rows, slot and position in flight while it works on this one's; a
-// gather has four tokens in flight.
+// Append.  A task is one token's q rows, or k and v rows of its kv heads, at most 4 KB.  The tasks are split
+// evenly into a span per warp, and a warp runs its own ring of bulk copies: a task's
+// rows are contiguous, and its row of the table comes along, so reads are in flight
+// without registers, three tasks deep.  A lane takes two units of 8 dims of a
+// row: with the half pairing a unit and its partner, so that each element is
+// widened once and no shuffle is needed; else neighbours, which are one block of
+// an E2M1 row.  (Rows held in registers instead, one unit a lane and the
+// partner by shuffle, one token ahead: 129 instructions per 32 units and 47 us where
+// this takes PLACEHOLDER.)
+//
+// Gather.  A lane takes one unit; a warp walks over tokens with one group of
+// rows, four tokens in flight.
 //
 // Divisions by a head scale h are x * (1 / h) corrected by one residual: with
 // y = RN(1 / h), q = RN(x y) and r = x - q h (exact in an fma), RN(q + r y) is the
@@ -22,6 +26,7 @@
 // falls below fp32's normal range; outside of a safe range the plain division runs.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "pa_common.cuh"
@@ -64,28 +69,32 @@ __device__ __forceinline__ float div_by(float x, float h, float y) {
   return fabsf(r) > 0.f ? __fmaf_rn(r, y, q) : q;
 }
 
-// Largest magnitude of 8 elements, NaN if one is NaN.
+// Largest magnitude of 8 packed elements, NaN if one is NaN.
 template <typename T>
 __device__ __forceinline__ float amax8(const uint32_t (&w)[4]) {
-  constexpr bool kHalf = std::is_same<T, __half>::value;
   auto top = [](uint32_t a, uint32_t b) {
     uint32_t r;
-    if constexpr (kHalf) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    if constexpr (std::is_same<T, __half>::value) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   };
   constexpr uint32_t kAbs = 0x7fff7fffu;
   const uint32_t m = top(top(w[0] & kAbs, w[1] & kAbs), top(w[2] & kAbs, w[3] & kAbs));
-  const float2 f = Elem<T>::to_f2(top(m, __byte_perm(m, 0, 0x1032)));
-  return f.x;
+  return Elem<T>::to_f2(top(m, __byte_perm(m, 0, 0x1032))).x;
 }
 
-// Head scales whose reciprocal and the products with it stay well inside fp32's range.
-__device__ __forceinline__ bool safe_scale(float h) { return h > 0x1p-60f && h < 0x1p60f; }
+// A kv head's scale, its reciprocal, and whether that and the products with it stay well inside fp32's range.
+struct HeadScale {
+  float h, y;
+  bool safe;
+};
+__device__ __forceinline__ HeadScale head_scale(float h) {
+  return HeadScale{h, __frcp_rn(h), h > 0x1p-60f && h < 0x1p60f};
+}
 
 // 8 elements -> 8 E4M3 codes of x / h, in two words.
 template <typename T>
-__device__ __forceinline__ uint2 e4m3x8_of(const uint32_t (&w)[4], float h, float y, bool safe) {
+__device__ __forceinline__ uint2 e4m3x8_of(const uint32_t (&w)[4], const HeadScale& s) {
   float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -94,13 +103,14 @@ __device__ __forceinline__ uint2 e4m3x8_of(const uint32_t (&w)[4], float h, floa
     f[2 * j + 1] = v.y;
   }
   // a quotient beyond fp32 (a bf16 row) must come out infinite, not NaN; fp16's are below 2^77
-  if (!std::is_same<T, __half>::value) safe = safe && !(amax8<T>(w) * y >= 0x1p100f);
+  bool safe = s.safe;
+  if (!std::is_same<T, __half>::value) safe = safe && !(amax8<T>(w) * s.y >= 0x1p100f);
   if (safe) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = div_by(f[j], h, y);
+    for (int j = 0; j < 8; ++j) f[j] = div_by(f[j], s.h, s.y);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], h);
+    for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], s.h);
   }
   uint32_t o[4];
 #pragma unroll
@@ -109,187 +119,264 @@ __device__ __forceinline__ uint2 e4m3x8_of(const uint32_t (&w)[4], float h, floa
   return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
 }
 
-// 8 elements of a block of 16 (two adjacent lanes) -> their E2M1 codes in a word, and the block's scale code.
-template <typename T>
-__device__ __forceinline__ uint32_t e2m1x8_of(const uint32_t (&w)[4], float h, float y, bool safe, uint8_t* scale) {
-  float amax = amax8<T>(w);
-  const float other = __shfl_xor_sync(0xffffffffu, amax, 1);
-  const bool nan = amax != amax || other != other;
-  amax = fmaxf(amax, other);
+// The scale code of a block of 16 dims with largest magnitude `amax` (NaN: a
+// dim is NaN): the E4M3 value nearest to (amax / 6) / h, 6 being E2M1's largest,
+// at most 448.  *r is the factor that takes a value to the codes' range.
+__device__ __forceinline__ uint8_t block_scale(float amax, const HeadScale& s, float* r) {
   float want;
-  if (safe && amax < 0x1p60f)  // below 2^-60 the scale is 0 either way
-    want = div_by(div_by(amax, 6.f, 0.16666667163372039795f), h, y);
+  if (s.safe && amax < 0x1p60f)  // what is too small for the correction gives a zero scale either way
+    want = div_by(div_by(amax, 6.f, 0.16666667163372039795f), s.h, s.y);
   else
-    want = __fdiv_rn(__fdiv_rn(amax, 6.f), h);
-  *scale = nan ? 0x7f : (uint8_t)__nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
-  const float f = e4m3_to_f(*scale);
-  const float r = f > 0.f ? __frcp_rn(__fmul_rn(f, h)) : 0.f;
-  uint32_t o[4];
+    want = __fdiv_rn(__fdiv_rn(amax, 6.f), s.h);
+  const uint8_t code = amax != amax ? 0x7f : (uint8_t)__nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
+  const float f = e4m3_to_f(code);
+  *r = f > 0.f ? __frcp_rn(__fmul_rn(f, s.h)) : 0.f;
+  return code;
+}
+
+// 8 elements times r -> 8 E2M1 codes: nearest, ties to the even code, saturating at 6.
+template <typename T>
+__device__ __forceinline__ uint32_t e2m1x8_of(const uint32_t (&w)[4], float r) {
+  float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 v = Elem<T>::to_f2(w[j]);
-    o[j] = e2m1x2_of(__fmul_rn(v.x, r), __fmul_rn(v.y, r));
+    f[2 * j] = __fmul_rn(v.x, r);
+    f[2 * j + 1] = __fmul_rn(v.y, r);
   }
-  return (o[0] | (o[1] << 8)) | ((o[2] | (o[3] << 8)) << 16);
+  uint32_t o;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(o)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return o;
 }
 
-template <typename T, int FMT, int D, int U>
-__global__ void __launch_bounds__(256, 3)
-rope_append_kernel(const RopeArgs a, const int num_tokens, const int slices, const FastDiv by_block) {
-  constexpr int UNITS = D / 8;        // lanes per row
-  constexpr int RW = 32 / UNITS;      // rows per warp and group
-  const int lane = threadIdx.x & 31, u = lane % UNITS;
-  const int kv_rows = a.num_q_heads + a.num_kv_heads, rows = kv_rows + a.num_kv_heads;
-  const int warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int step = gridDim.x * (blockDim.x >> 5) / slices;  // tokens between a warp's
-  const int slice = warp % slices;
-  int t = warp / slices;
-  if (t >= step) t = num_tokens;  // a warp over
+constexpr int kRowWarps = 4, kRowStages = 3, kRowCtas = 4;
+constexpr int kTaskBytes = 4096, kStageBytes = kTaskBytes + 512;  // rows, then the table's row
+
+template <typename T, int FMT, int D>
+__global__ void __launch_bounds__(kRowWarps * 32, kRowCtas)
+rope_append_kernel(const RopeArgs a, const int num_tokens, const FastDiv by_block) {
+  constexpr int LANES = D / 16, RW = 32 / LANES;   // lanes per row, rows per step
+  constexpr int PR = kTaskBytes / (2 * D);         // rows of a task
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, p = lane % LANES;
+  unsigned char* stages = smem + warp * kRowStages * kStageBytes;
+  const uint32_t bar0 = smem_addr(smem) + kRowWarps * kRowStages * kStageBytes + warp * kRowStages * 8;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kRowStages; ++i) mbar_init(bar0 + i * 8, 1);
+    mbar_init_fence();
+  }
+  __syncwarp();
   pdl_wait();  // a copy-on-write of this slot's block must land first
   pdl_launch_dependents();
-  if (t >= num_tokens) return;
 
-  // this thread's rows: 16 bytes of one head's row of q, k or v
-  struct Row {
-    const uint16_t* src;
-    unsigned char* dst;  // of token 0 (q) or slot 0 (k, v); null: no such row
-    long long src_step;
-    float h, y;          // head scale and its reciprocal
-    bool is_q, is_v;
-  } row[U];
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int r = (slice * U + i) * RW + lane / UNITS;
-    Row& w = row[i];
-    w.is_q = r < a.num_q_heads;
-    w.is_v = r >= kv_rows;
-    const int head = w.is_q ? r : w.is_v ? r - kv_rows : r - a.num_q_heads;
-    const bool live = r < rows;
-    const long long stride = w.is_q ? a.q_stride : w.is_v ? a.v_stride : a.k_stride;
-    w.src = (w.is_q ? a.q : w.is_v ? a.v : a.k) + t * stride + (live ? head * D + u * 8 : 0);
-    w.src_step = step * stride;
-    unsigned char* pool = static_cast<unsigned char*>(w.is_v ? a.v_cache : a.k_cache);
-    if (w.is_q) w.dst = reinterpret_cast<unsigned char*>(a.q_out + head * D + u * 8);
-    else if (FMT == kFmt16) w.dst = pool + (head * D + u * 8) * 2;
-    else if (FMT == kFmtFp8) w.dst = pool + head * D + u * 8;
-    else w.dst = pool + head * fp4_head_bytes(a.block_size, D);
-    if (!live) w.dst = nullptr;
-    w.h = FMT == kFmt16 || w.is_q || !live ? 1.f : __ldg((w.is_v ? a.v_scale : a.k_scale) + head);
-    w.y = __frcp_rn(w.h);
-  }
-  const bool rot_unit = u * 8 < a.rotary_dim;
-  const long long kv_bytes = (long long)a.num_kv_heads * D;
-  struct Token {
-    uint4 x[U];
-    int slot, pos;
-  };
-  auto load = [&](int at) {
-    Token n;
-    n.slot = __ldg(a.slot_mapping + at);
-    n.pos = a.rotary_dim > 0 ? __ldg(a.positions + at) : 0;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      n.x[i] = *reinterpret_cast<const uint4*>(row[i].src);
-      row[i].src += row[i].src_step;
-    }
-    return n;
-  };
+  const int num_slots = (int)a.num_slots;  // below 2^31
+  // tasks of a token: PR of its q rows, or half as many of k and of v
+  const int q_tasks = (a.num_q_heads + PR - 1) / PR;
+  const int per_token = q_tasks + (a.num_kv_heads + PR / 2 - 1) / (PR / 2);
+  const long long total = (long long)num_tokens * per_token, warps = (long long)gridDim.x * kRowWarps;
+  const long long w = (long long)blockIdx.x * kRowWarps + warp;
+  const long long begin = total * w / warps;
+  const int n_mine = (int)(total * (w + 1) / warps - begin);
+  if (n_mine == 0) return;
 
-  for (Token next = load(t); t < num_tokens; t += step) {
-    const Token now = next;
-    bool skip = now.slot < 0;  // padding
-    if (now.slot >= a.num_slots) {
-      if (slice == 0 && lane == 0) report(a.err, kErrSlot);
-      skip = true;
-    } else if (!skip && a.rotary_dim > 0 && (unsigned)now.pos >= (unsigned)a.max_position) {
-      if (slice == 0 && lane == 0) report(a.err, kErrPosition);
-      skip = true;
+  // The copies run kRowStages tasks ahead: their cursor, and the slots of the tasks in flight (negative: skip).
+  int f_t = (int)(begin / per_token), f_part = (int)(begin % per_token), f_stage = 0;
+  int slots[kRowStages];
+  // first head of a task, and the number of heads
+  auto head_of = [&](int part) { return part < q_tasks ? part * PR : (part - q_tasks) * (PR / 2); };
+  auto heads_of = [&](int part) {
+    return part < q_tasks ? min(PR, a.num_q_heads - part * PR) : min(PR / 2, a.num_kv_heads - (part - q_tasks) * (PR / 2));
+  };
+  // Starts the next task's copies and returns its slot, or -1 where the token is
+  // skipped; what is wrong with a token is reported with its first task.
+  auto issue = [&](int slot, int pos) {
+    const bool padding = slot < 0, bad_slot = slot >= num_slots;
+    const bool bad_pos = a.rotary_dim > 0 && (unsigned)pos >= (unsigned)a.max_position;
+    if (padding || bad_slot || bad_pos) {
+      if (!padding && f_part == 0 && lane == 0) report(a.err, bad_slot ? kErrSlot : kErrPosition);
+      slot = -1;
     }
-    // cos and (signed) sin of this thread's 8 dims, and the lane of its partner unit
-    float cs[8], sn[8];
-    int partner = lane;
-    if (!skip && rot_unit) {
-      const float* tab = a.cos_sin + (long long)now.pos * a.rotary_dim;
-      const int half = a.rotary_dim / 2;
-      if (a.interleaved) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(tab + u * 4));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(tab + half + u * 4));
-        cs[0] = cs[1] = c.x; cs[2] = cs[3] = c.y; cs[4] = cs[5] = c.z; cs[6] = cs[7] = c.w;
-        sn[0] = -s.x; sn[1] = s.x; sn[2] = -s.y; sn[3] = s.y;
-        sn[4] = -s.z; sn[5] = s.z; sn[6] = -s.w; sn[7] = s.w;
-      } else {
-        const int hu = half / 8;      // units per half
-        const bool lower = u < hu;
-        partner = lower ? lane + hu : lane - hu;
-        const float* c = tab + (lower ? u : u - hu) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 cv = __ldg(reinterpret_cast<const float4*>(c + i));
-          const float4 sv = __ldg(reinterpret_cast<const float4*>(c + half + i));
-          cs[i] = cv.x; cs[i + 1] = cv.y; cs[i + 2] = cv.z; cs[i + 3] = cv.w;
-          sn[i] = lower ? -sv.x : sv.x; sn[i + 1] = lower ? -sv.y : sv.y;
-          sn[i + 2] = lower ? -sv.z : sv.z; sn[i + 3] = lower ? -sv.w : sv.w;
+    const bool is_q = f_part < q_tasks;
+    const uint32_t bytes = slot < 0 ? 0 : heads_of(f_part) * D * 2;
+    const uint32_t table_bytes = slot < 0 ? 0 : a.rotary_dim * 4;
+    if (lane == 0) {
+      const uint32_t bar = bar0 + f_stage * 8, dst = smem_addr(stages + f_stage * kStageBytes);
+      const int from = head_of(f_part) * D;
+      mbar_arrive_expect_tx(bar, (is_q ? bytes : 2 * bytes) + table_bytes);
+      if (bytes) {
+        if (is_q) {
+          bulk_load(dst, a.q + f_t * a.q_stride + from, bytes, bar);
+        } else {
+          bulk_load(dst, a.k + f_t * a.k_stride + from, bytes, bar);
+          bulk_load(dst + kTaskBytes / 2, a.v + f_t * a.v_stride + from, bytes, bar);
         }
+        if (table_bytes) bulk_load(dst + kTaskBytes, a.cos_sin + (long long)pos * a.rotary_dim, table_bytes, bar);
       }
     }
-    if (t + step < num_tokens) next = load(t + step);
-    if (skip) continue;
-    // where the token's rows start: q's, and the pools' (codes and scales apart in an E2M1 pool)
-    const long long q_at = t * a.q_out_stride * 2;
-    long long kv_at, sc_at = 0;
-    if constexpr (FMT == kFmtFp4) {
-      const int block = by_block.div(now.slot), off = now.slot - block * a.block_size;
-      kv_at = block * (kv_bytes * a.block_size / 16 * 9);
-      sc_at = kv_at + (long long)a.block_size * (D / 2) + off * (D / 16) + u / 2;
-      kv_at += off * (D / 2) + u * 4;
-    } else {
-      kv_at = now.slot * (FMT == kFmt16 ? 2 * kv_bytes : kv_bytes);
-    }
+    if (++f_part == per_token) { f_part = 0; ++f_t; }
+    if (++f_stage == kRowStages) f_stage = 0;
+    return slot;
+  };
+  auto slot_of = [&](int t) { return __ldg(a.slot_mapping + t); };
+  auto pos_of = [&](int t) { return a.rotary_dim > 0 ? __ldg(a.positions + t) : 0; };
+  int t = f_t, part = f_part, stage_at = 0, phase = 0;  // the task at work
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const Row& w = row[i];
-      uint4 y = now.x[i];
-      if (a.rotary_dim > 0) {
-        uint4 p;
-        if (a.interleaved) {
-          p = make_uint4(__byte_perm(y.x, 0, 0x1032), __byte_perm(y.y, 0, 0x1032), __byte_perm(y.z, 0, 0x1032),
-                         __byte_perm(y.w, 0, 0x1032));
-        } else {
-          p = make_uint4(__shfl_sync(0xffffffffu, y.x, partner), __shfl_sync(0xffffffffu, y.y, partner),
-                         __shfl_sync(0xffffffffu, y.z, partner), __shfl_sync(0xffffffffu, y.w, partner));
-        }
-        if (rot_unit && !w.is_v) {
-          const uint32_t xw[4] = {y.x, y.y, y.z, y.w}, pw[4] = {p.x, p.y, p.z, p.w};
-          uint32_t yw[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 xf = Elem<T>::to_f2(xw[j]), pf = Elem<T>::to_f2(pw[j]);
-            yw[j] = pack2<T>(__fadd_rn(__fmul_rn(xf.x, cs[2 * j]), __fmul_rn(pf.x, sn[2 * j])),
-                             __fadd_rn(__fmul_rn(xf.y, cs[2 * j + 1]), __fmul_rn(pf.y, sn[2 * j + 1])));
-          }
-          y = make_uint4(yw[0], yw[1], yw[2], yw[3]);
-        }
+  for (int k = 0; k < kRowStages; ++k) slots[k] = k < n_mine ? issue(slot_of(f_t), pos_of(f_t)) : -1;
+  int next_slot = 0, next_pos = 0;
+  if (kRowStages < n_mine) next_slot = slot_of(f_t), next_pos = pos_of(f_t);
+
+  // bytes from a token, a block, or a head to the next
+  const long long kv_row = (long long)a.num_kv_heads * D * (FMT == kFmt16 ? 2 : 1);
+  const long long run = fp4_head_bytes(a.block_size, D), block_bytes = run * a.num_kv_heads;
+  for (int k = 0; k < n_mine; ++k) {
+    if (!mbar_wait(bar0 + stage_at * 8, phase, a.err)) {
+      for (int i = k + 1; i < min(n_mine, k + kRowStages); ++i) {  // let the copies in flight land
+        if (++stage_at == kRowStages) { stage_at = 0; phase ^= 1; }
+        mbar_wait(bar0 + stage_at * 8, phase, a.err);
       }
-      if (w.is_q) *reinterpret_cast<uint4*>(w.dst + q_at) = y;
-      if (__all_sync(0xffffffffu, w.is_q)) continue;
-      const bool store = w.dst && !w.is_q;
-      if constexpr (FMT == kFmt16) {
-        if (store) *reinterpret_cast<uint4*>(w.dst + kv_at) = y;
-      } else {
-        const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-        if constexpr (FMT == kFmtFp8) {
-          const uint2 o = e4m3x8_of<T>(yw, w.h, w.y, safe_scale(w.h));
-          if (store) *reinterpret_cast<uint2*>(w.dst + kv_at) = o;
-        } else {
-          uint8_t sc;
-          const uint32_t o = e2m1x8_of<T>(yw, w.h, w.y, safe_scale(w.h), &sc);
-          if (store) {
-            *reinterpret_cast<uint32_t*>(w.dst + kv_at) = o;
-            if ((u & 1) == 0) w.dst[sc_at] = sc;
+      return;
+    }
+    const int slot = slots[0];
+    const unsigned char* stage = stages + stage_at * kStageBytes;
+    if (slot >= 0) {
+      const bool is_q = part < q_tasks;
+      const int head0 = head_of(part), heads = heads_of(part);
+#pragma unroll 1
+      for (int is_v = 0; is_v < (is_q ? 1 : 2); ++is_v) {
+        // this lane's two units: a unit and its partner (half pairing), else neighbours
+        const int hu = is_v || a.interleaved ? 0 : a.rotary_dim / 16;  // units per half
+        const bool split = p < hu, turn = split || (!is_v && a.interleaved && p * 16 < a.rotary_dim);
+        const int u0 = split ? p : hu + p + (p - hu), u1 = split ? p + hu : u0 + 1;
+        // half pairing: cos and sin of the pairs (unit, partner); interleaved: of the 4 pairs of u0, then of u1
+        alignas(16) float cs[8], sn[8];
+        if (turn) {
+          const float* tab = reinterpret_cast<const float*>(stage + kTaskBytes) + p * 8;
+#pragma unroll
+          for (int i = 0; i < 8; i += 4) {
+            *reinterpret_cast<float4*>(cs + i) = *reinterpret_cast<const float4*>(tab + i);
+            *reinterpret_cast<float4*>(sn + i) = *reinterpret_cast<const float4*>(tab + a.rotary_dim / 2 + i);
           }
         }
+        // this lane's row of the first step: in the stage, its head's scale, and where it goes (rows; block scales)
+        const int row = lane / LANES, head = head0 + row;
+        const unsigned char* rows = stage + is_v * (kTaskBytes / 2) + row * (2 * D);
+        const float* scale = (is_v ? a.v_scale : a.k_scale) + head;
+        unsigned char* to = static_cast<unsigned char*>(is_v ? a.v_cache : a.k_cache);
+        unsigned char* to_scale = nullptr;
+        long long to_step;
+        if (is_q) {
+          to = reinterpret_cast<unsigned char*>(a.q_out + t * a.q_out_stride + head * D);
+          to_step = RW * D * 2;
+        } else if constexpr (FMT == kFmtFp4) {
+          const int block = by_block.div(slot), off = slot - block * a.block_size;
+          to += block * block_bytes + head * run;
+          to_scale = to + a.block_size * (D / 2) + off * (D / 16);
+          to += off * (D / 2);
+          to_step = RW * run;
+        } else {
+          to += slot * kv_row + head * (FMT == kFmt16 ? 2 * D : D);
+          to_step = RW * (FMT == kFmt16 ? 2 * D : D);
+        }
+        // all lanes take every step (the shuffles below need them); rows past the task's are computed and dropped
+#pragma unroll 2
+        for (int i = 0; i < heads; i += RW, rows += RW * 2 * D, scale += RW, to += to_step) {
+          const bool live = i + row < heads;
+          const uint4 x0 = *reinterpret_cast<const uint4*>(rows + u0 * 16);
+          const uint4 x1 = *reinterpret_cast<const uint4*>(rows + u1 * 16);
+          uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+          if (turn) {
+            if (a.interleaved) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 v = Elem<T>::to_f2(w0[j]), z = Elem<T>::to_f2(w1[j]);
+                w0[j] = pack2<T>(__fsub_rn(__fmul_rn(v.x, cs[j]), __fmul_rn(v.y, sn[j])),
+                                 __fadd_rn(__fmul_rn(v.y, cs[j]), __fmul_rn(v.x, sn[j])));
+                w1[j] = pack2<T>(__fsub_rn(__fmul_rn(z.x, cs[4 + j]), __fmul_rn(z.y, sn[4 + j])),
+                                 __fadd_rn(__fmul_rn(z.y, cs[4 + j]), __fmul_rn(z.x, sn[4 + j])));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 v = Elem<T>::to_f2(w0[j]), z = Elem<T>::to_f2(w1[j]);
+                w0[j] = pack2<T>(__fsub_rn(__fmul_rn(v.x, cs[2 * j]), __fmul_rn(z.x, sn[2 * j])),
+                                 __fsub_rn(__fmul_rn(v.y, cs[2 * j + 1]), __fmul_rn(z.y, sn[2 * j + 1])));
+                w1[j] = pack2<T>(__fadd_rn(__fmul_rn(z.x, cs[2 * j]), __fmul_rn(v.x, sn[2 * j])),
+                                 __fadd_rn(__fmul_rn(z.y, cs[2 * j + 1]), __fmul_rn(v.y, sn[2 * j + 1])));
+              }
+            }
+          }
+          if (FMT == kFmt16 || is_q) {
+            uint4* out = reinterpret_cast<uint4*>(to);
+            if (live) {
+              out[u0] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+              out[u1] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+            }
+          } else if constexpr (FMT == kFmtFp8) {
+            const HeadScale s = head_scale(live ? __ldg(scale) : 1.f);
+            const uint2 o0 = e4m3x8_of<T>(w0, s), o1 = e4m3x8_of<T>(w1, s);
+            uint2* out = reinterpret_cast<uint2*>(to);
+            if (live) {
+              out[u0] = o0;
+              out[u1] = o1;
+            }
+          } else if constexpr (FMT == kFmtFp4) {
+            const HeadScale s = head_scale(live ? __ldg(scale) : 1.f);
+            const float m0 = amax8<T>(w0), m1 = amax8<T>(w1);
+            uint32_t* codes = reinterpret_cast<uint32_t*>(to);
+            auto larger = [](float x, float y) { return x != x ? x : y != y ? y : fmaxf(x, y); };
+            if (hu == 0) {  // neighbours: one block
+              float f;
+              const uint8_t sc = block_scale(larger(m0, m1), s, &f);
+              const uint32_t o0 = e2m1x8_of<T>(w0, f), o1 = e2m1x8_of<T>(w1, f);
+              if (live) {
+                *reinterpret_cast<uint2*>(codes + u0) = make_uint2(o0, o1);
+                to_scale[p] = sc;
+              }
+            } else {
+              // the other unit of each unit's block: in lane `l` of this row, as its first or second unit
+              auto mate = [&](int u) {
+                const int v = u ^ 1, l = v < hu ? v : v < 2 * hu ? v - hu : hu + (v - 2 * hu) / 2;
+                const int src = lane - p + l;
+                const float f0 = __shfl_sync(0xffffffffu, m0, src), f1 = __shfl_sync(0xffffffffu, m1, src);
+                return v < hu || (v >= 2 * hu && (v & 1) == 0) ? f0 : f1;
+              };
+              const float n0 = mate(u0), n1 = mate(u1);
+              float f0, f1;
+              const uint8_t s0 = block_scale(larger(m0, n0), s, &f0), s1 = block_scale(larger(m1, n1), s, &f1);
+              const uint32_t o0 = e2m1x8_of<T>(w0, f0), o1 = e2m1x8_of<T>(w1, f1);
+              if (live) {
+                codes[u0] = o0;
+                codes[u1] = o1;
+                if ((u0 & 1) == 0) to_scale[u0 / 2] = s0;
+                if ((u1 & 1) == 0) to_scale[u1 / 2] = s1;
+              }
+            }
+            to_scale += to_step;
+          }
+        }
       }
     }
+    __syncwarp();
+    // the stage is free again: refill it
+    int refill = -1;
+    if (k + kRowStages < n_mine) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      refill = issue(next_slot, next_pos);
+      if (k + kRowStages + 1 < n_mine) next_slot = slot_of(f_t), next_pos = pos_of(f_t);
+    }
+#pragma unroll
+    for (int i = 0; i + 1 < kRowStages; ++i) slots[i] = slots[i + 1];
+    slots[kRowStages - 1] = refill;
+    if (++part == per_token) { part = 0; ++t; }
+    if (++stage_at == kRowStages) { stage_at = 0; phase ^= 1; }
   }
 }
 
@@ -389,10 +476,16 @@ unsigned row_ctas(long long warps, int warps_per_token, int per_sm) {
 
 template <typename T, int FMT, int D>
 cudaError_t launch_append(const RopeArgs& a, int num_tokens, cudaStream_t stream) {
-  constexpr int U = 2;
-  const int rw = 256 / D, groups = (a.num_q_heads + 2 * a.num_kv_heads + rw - 1) / rw, slices = (groups + U - 1) / U;
-  return launch_pdl(rope_append_kernel<T, FMT, D, U>, dim3(row_ctas((long long)num_tokens * slices, slices, 3)), dim3(256),
-                    0, stream, a, num_tokens, slices, FastDiv(a.block_size));
+  constexpr int smem = kRowWarps * kRowStages * (kStageBytes + 8), PR = kTaskBytes / (2 * D);
+  auto* kern = rope_append_kernel<T, FMT, D>;
+  static std::atomic<uint64_t> configured{0};
+  const cudaError_t e = allow_smem(kern, smem, &configured);
+  if (e != cudaSuccess) return e;
+  const long long tasks =
+      (long long)num_tokens * ((a.num_q_heads + PR - 1) / PR + (a.num_kv_heads + PR / 2 - 1) / (PR / 2));
+  const long long ctas = (tasks + kRowWarps - 1) / kRowWarps, wave = 148 * kRowCtas;  // what a B200 holds at once
+  return launch_pdl(kern, dim3((unsigned)(ctas < wave ? ctas : wave)), dim3(kRowWarps * 32), smem, stream, a, num_tokens,
+                    FastDiv(a.block_size));
 }
 
 template <typename T, int FMT, int D>
