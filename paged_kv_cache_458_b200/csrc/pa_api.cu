@@ -193,19 +193,16 @@ long long workspace_parts(const pa_shape* s, int32_t max_context_len) {
   return P > 1 ? P : 0;
 }
 
-// Workspace of the E2M1 decode, in bytes: per worker two partials of `group` rows
-// in fp32, their (max, sum) pairs, and the spans of every (sequence, kv head).
+// Workspace of the E2M1 decode: two partial states per worker, then a word per worker.
 struct Fp4Workspace {
   pa::Fp4Split split;
-  long long ml, parts, bytes;  // offsets; the rows are at 0
+  long long arrivals, bytes;  // offset of the words; all of it
 };
 Fp4Workspace fp4_workspace(const pa_shape* s, int32_t max_context_len) {
   Fp4Workspace w;
   pa::fp4_decode_split(s->num_seqs, s->num_kv_heads, max_context_len, s->partition_tokens, &w.split);
-  const long long rows = 2LL * w.split.workers * (s->num_q_heads / s->num_kv_heads);
-  w.ml = round256(rows * s->head_dim * 4);
-  w.parts = w.ml + round256(rows * 8);
-  w.bytes = w.parts + round256(8LL * s->num_seqs * s->num_kv_heads) + 256;
+  w.arrivals = 2LL * w.split.workers * pa::fp4_state_bytes(s->head_dim, s->num_q_heads / s->num_kv_heads);
+  w.bytes = w.arrivals + 8LL * w.split.workers;
   return w;
 }
 
@@ -780,11 +777,10 @@ pa_status pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
   a.block_tables = block_tables;
   a.context_lens = context_lens;
   a.out = static_cast<uint16_t*>(out);
-  a.ws_acc = reinterpret_cast<float*>(ws);
-  a.ws_ml = reinterpret_cast<float*>(ws + w.ml);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
+  a.epoch = next_epochs(1);
   a.num_seqs = shape->num_seqs;
   a.num_q_heads = shape->num_q_heads;
   a.num_kv_heads = shape->num_kv_heads;
@@ -796,8 +792,8 @@ pa_status pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
   a.err = error_word();
   if (!a.err) return cuda_failed("device error word lookup failed");
   int launched = 0;
-  cudaError_t ce = pa::launch_decode_fp4(a, shape->dtype, shape->head_dim, k_cache, v_cache, w.split,
-                                         reinterpret_cast<int2*>(ws + w.parts),
+  cudaError_t ce = pa::launch_decode_fp4(a, shape->dtype, shape->head_dim, k_cache, v_cache, w.split, ws,
+                                         reinterpret_cast<unsigned long long*>(ws + w.arrivals),
                                          reinterpret_cast<cudaStream_t>(stream), &launched);
   count_launches(launched);
   return ce == cudaSuccess ? PA_OK : cuda_failed(ce);

@@ -3,13 +3,22 @@
 // Work split.  An item is a (sequence, kv head) pair; its context is cut into chunks of
 // 64 tokens.  The chunks of all items, in order, are split evenly into one span
 // per worker: long and short contexts balance, and only an item cut by a
-// span's border needs merging.  Every CTA finds its spans itself, by a scan
-// over the context lengths.  A worker is a warp, or (few long items) the four
-// warps of a CTA, which take a span's chunks in turn and merge through shared
-// memory at an item's end.  A warp runs its own ring of bulk copies, across
-// items: a (block, head) run is contiguous, so a chunk of K is one copy per
-// block (two where a block holds more than the copy: codes, then block scales),
-// one lane each, and table entries are read one chunk ahead.
+// span's border needs merging.  A worker is a warp; or, where there are fewer
+// items than CTAs, a team: the four warps of a CTA, which claim a span's chunks
+// one by one and merge through shared memory at an item's end.  (Warps of one SM
+// differ by 10 percent in what they get through; a team evens that out, and
+// cuts an item into a quarter of the parts.)  A worker finds its span by a scan over the
+// context lengths.  A warp runs its own ring of bulk copies, across items: a
+// (block, head) run is contiguous, so a chunk of K is one copy per block (two
+// where a block holds more than the copy: codes, then block scales), one lane
+// each, and table entries are read one chunk ahead.
+//
+// A cut item's parts are merged as they arrive: the parts form a tree of 8
+// children a node; a worker publishes its partial result, counts itself in at the
+// node, and the last one in combines the children, in order, and goes on to the
+// node above with the result, so the outcome does not depend on who came
+// last.  Nobody waits.  (A kernel of its own for this cost 8 to 12 us at 64 to 128
+// sequences: its loads start only when the last span has ended.)
 //
 // Both products run as m16n8k16 matrix instructions in f16 with fp32 sums, the
 // cache always on the 16-row side and the group's query heads on the 8-column side:
@@ -48,32 +57,32 @@
 namespace pa {
 
 constexpr int kFp4Warps = 4;
-#ifndef FP4_CT
-#define FP4_CT 64
-#define FP4_NST 2
-#endif
-constexpr int kFp4Chunk = FP4_CT;  // tokens a stage holds
-#ifndef FP4_CTAS
-#define FP4_CTAS 3
-#endif
-#ifndef FP4_TEAM
-#define FP4_TEAM 1000
-#endif
-constexpr int kFp4Ctas = FP4_CTAS;    // per SM, by registers and (D = 128) shared memory
+constexpr int kFp4Chunk = 64;   // tokens a stage holds
+constexpr int kFp4Stages = 2;   // per warp
+constexpr int kFp4Ctas = 3;     // per SM, by registers and (D = 128) shared memory
+constexpr int kFp4Radix = 8;    // children of a merge node
 
-template <int D, int GT>
+template <int D>
 struct Fp4Smem {
-  static constexpr int kStages = FP4_NST;
   static constexpr int kTokenBytes = D * 9 / 16;
   static constexpr int kPoolBytes = kFp4Chunk * kTokenBytes;  // K or V of one stage
   static constexpr int kStageBytes = 2 * kPoolBytes;
-  static constexpr int kBars = kFp4Warps * kStages * kStageBytes;
-  static constexpr int kScan = kBars + kFp4Warps * kStages * 8;
-  static constexpr int kTotal = kScan + 32;
-  static constexpr int kStateBytes = ((GT == 4 ? D / 32 : D / 16) + 1) * (GT == 16 ? 2 : 1) * 32 * 16;  // one warp's, to merge
-  static constexpr int kMerge = kScan + 32;
-  static constexpr int kTotalMerge = kMerge + 3 * kStateBytes;
+  static constexpr int kBars = kFp4Warps * kFp4Stages * kStageBytes;
+  static constexpr int kTeam = kBars + kFp4Warps * kFp4Stages * 8;  // next chunk to claim; merge verdict
+  static constexpr int kTotal = kTeam + 16;
 };
+
+// A warp's state as it is stored: GT columns of D dims (4 or 8 columns a tile), maxima and sums.
+template <int D, int GT>
+struct Fp4State {
+  static constexpr int NT = GT == 16 ? 2 : 1;                // column tiles of 8
+  static constexpr int MT = GT == 4 ? D / 32 : D / 16;       // 16-row tiles of output dims, or of pairs of dims
+  static constexpr int kBytes = (MT + 1) * NT * 32 * 16;
+};
+int fp4_state_bytes(int head_dim, int group) {
+  if (head_dim == 128) return group <= 4 ? Fp4State<128, 4>::kBytes : group <= 8 ? Fp4State<128, 8>::kBytes : Fp4State<128, 16>::kBytes;
+  return group <= 4 ? Fp4State<64, 4>::kBytes : group <= 8 ? Fp4State<64, 8>::kBytes : Fp4State<64, 16>::kBytes;
+}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -104,19 +113,19 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// GT: the group's query heads, at most: 4, 8 or 16.  R: tokens of one copy.
-template <typename T, int D, int GT, int R>
+// GT: the group's query heads, at most: 4, 8 or 16.  R: tokens of one copy.  TEAM: the CTA's warps share a span.
+template <typename T, int D, int GT, int R, bool TEAM>
 __global__ void __launch_bounds__(kFp4Warps * 32, kFp4Ctas)
 decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
-                  const unsigned char* __restrict__ v_pool, const int num_workers, const int team, int2* item_parts) {
-  constexpr int NT = GT == 16 ? 2 : 1;  // column tiles of 8
+                  const unsigned char* __restrict__ v_pool, const int num_workers, float4* partials,
+                  unsigned long long* arrivals) {
+  constexpr int NT = Fp4State<D, GT>::NT, MT = Fp4State<D, GT>::MT;
   constexpr bool kPairs = GT == 4;      // V registers hold pairs of dims (see above), else pairs of tokens
-  using L = Fp4Smem<D, GT>;
+  using L = Fp4Smem<D>;
   constexpr bool kLo = std::is_same<T, __half>::value;  // p as hi + lo
-  constexpr int NW = kFp4Warps, NST = L::kStages, CT = kFp4Chunk, TILES = 2;
+  constexpr int NW = kFp4Warps, NST = kFp4Stages, CT = kFp4Chunk, TILES = 2;
   constexpr int KW = D / 32;   // words of K codes a thread takes per row
   constexpr int VW = D / 64;   // words of V codes a thread takes per row
-  constexpr int MT = kPairs ? VW * 2 : VW * 4;  // 16-row tiles of output dims, or of pairs of dims
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   unsigned char* stages = smem + warp * NST * L::kStageBytes;
@@ -131,73 +140,57 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   pdl_wait();  // the append before this decode must have landed
   pdl_launch_dependents();
 
-  // ---- this worker's span of chunks, and the sequence it starts in
+  // ---- this warp's span of chunks, and the sequence it starts in
   const int S = a.num_seqs, Hkv = a.num_kv_heads, G = a.group;
-  const bool alone = team == 1;
-  const int rank = alone ? 0 : warp, worker = alone ? blockIdx.x + gridDim.x * warp : blockIdx.x;
+  const int worker = TEAM ? blockIdx.x : blockIdx.x + gridDim.x * warp;
   auto context = [&](int s) { return max(0, min(__ldg(a.context_lens + s), a.max_context_len)); };
-  int span_begin = 0, span_end = 0, chunks, workers, seq = 0, seq_base = 0;  // seq_base: number of seq's first chunk
-  {
-    int* sh = reinterpret_cast<int*>(smem + L::kScan);
-    const int per = (S + NW * 32 - 1) / (NW * 32), lo = min(S, (int)threadIdx.x * per), hi = min(S, lo + per);
-    int sum = 0;
-    bool bad = false;
-    for (int s = lo; s < hi; ++s) {
-      sum += (context(s) + CT - 1) / CT;
-      const int c = __ldg(a.context_lens + s);
-      bad |= c < 0 || c > a.max_context_len;
+  int sum = 0;
+  bool bad = false;
+#pragma unroll 4
+  for (int s = lane; s < S; s += 32) {
+    const int c = __ldg(a.context_lens + s);
+    bad |= c < 0 || c > a.max_context_len;
+    sum += (max(0, min(c, a.max_context_len)) + CT - 1) / CT;
+  }
+  if (bad && blockIdx.x == 0 && warp == 0) report(a.err, kErrContextLen);
+  const int chunks = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum) * Hkv;  // below 2^31
+  const int workers = min(num_workers, chunks);  // so that no span among them is empty
+  // sequences without tokens: zero rows
+  for (int s = blockIdx.x + gridDim.x * warp; s < S; s += gridDim.x * NW)
+    if (context(s) == 0) {
+      uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)s * a.num_q_heads * D);
+      for (int i = lane; i < a.num_q_heads * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
     }
-    if (bad && blockIdx.x == 0) report(a.err, kErrContextLen);
-    int upto = sum;
+  if (worker >= workers) return;
+  const int span_begin = (int)((long long)chunks * worker / workers);
+  const int span_end = (int)((long long)chunks * (worker + 1) / workers);
+  // opens this span's arrival word: no count of another call is above the tag, and one of this call's stays
+  const unsigned long long tag = a.epoch << 8;
+  if (lane == 0) atomicMax(arrivals + worker, tag);
+  int* claims = reinterpret_cast<int*>(smem + L::kTeam);
+  if constexpr (TEAM) {
+    if (threadIdx.x == 0) claims[0] = span_begin;
+    __syncthreads();
+  }
+  // the sequence of chunk span_begin, and the number of its first chunk: 32 sequences at a time
+  int seq = 0, seq_base = 0;
+  for (;; seq += 32) {
+    const int n = seq + lane < S ? (context(seq + lane) + CT - 1) / CT * Hkv : 0;
+    int upto = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += v;
     }
-    if (lane == 31) sh[warp] = upto;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      if (w < warp) upto += sh[w];
-      total += sh[w];
+    const unsigned after = __ballot_sync(0xffffffffu, span_begin < seq_base + upto);
+    if (after) {
+      const int l = __ffs(after) - 1;
+      seq += l;
+      seq_base += __shfl_sync(0xffffffffu, upto - n, l);
+      break;
     }
-    chunks = total * Hkv;                // below 2^31
-    workers = min(num_workers, chunks);  // so that no span among them is empty
-    // every thread looks for the spans that start in its sequences
-    __syncthreads();
-    for (int w = 0; w < NW / team; ++w) {
-      const int id = alone ? blockIdx.x + gridDim.x * w : blockIdx.x;
-      if (id >= workers) break;
-      const int begin = (int)((long long)chunks * id / workers);
-      int before = upto - sum;
-      if (before * Hkv <= begin && begin < upto * Hkv) {
-        int s = lo;
-        for (;; ++s) {
-          const int n = (context(s) + CT - 1) / CT;
-          if (begin < (before + n) * Hkv) break;
-          before += n;
-        }
-        sh[2 * w] = s;
-        sh[2 * w + 1] = before * Hkv;
-      }
-    }
-    __syncthreads();
-    if (worker < workers) {
-      span_begin = (int)((long long)chunks * worker / workers);
-      span_end = (int)((long long)chunks * (worker + 1) / workers);
-      seq = sh[alone ? 2 * warp : 0];
-      seq_base = sh[alone ? 2 * warp + 1 : 1];
-    }
+    seq_base += __shfl_sync(0xffffffffu, upto, 31);
   }
-  // sequences without tokens: zero rows
-  for (int s = blockIdx.x; s < S; s += gridDim.x)
-    if (context(s) == 0) {
-      uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)s * a.num_q_heads * D);
-      for (int i = threadIdx.x; i < a.num_q_heads * D / 8; i += NW * 32) o[i] = make_uint4(0, 0, 0, 0);
-    }
-  if (span_begin >= span_end) return;  // a whole team returns
-  const int n_mine = max(0, (span_end - span_begin - rank + team - 1) / team);  // chunks of this warp
 
   // ---- copies: lane (sub, piece, pool) moves one piece of one group of R tokens, which never crosses a block
   const int bs = a.block_size;
@@ -209,56 +202,76 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   const long long run_bytes = fp4_head_bytes(bs, D);
   const unsigned char* c_base = ((lane & 1) ? v_pool : k_pool) + (c_piece ? bs * (D / 2) : 0);
   const int c_unit = c_piece ? D / 16 : D / 2;
-  // The copies' cursor: the next chunk to fetch, its item and chunk number there;
-  // this lane's group in it: first token, its table index and offset in the block.
-  int f_left = n_mine, f_seq = seq, f_head = 0, f_chunk = 0, f_ctx = context(seq), f_idx = 0, f_off = 0;
-  const int step_idx = team * CT / bs, step_off = team * CT - step_idx * bs;
-  {
-    int rel = span_begin + rank - seq_base;
-    int n = (f_ctx + CT - 1) / CT;
-    while (f_left > 0 && rel >= n * Hkv) {
-      rel -= n * Hkv;
-      f_ctx = context(++f_seq);
-      n = (f_ctx + CT - 1) / CT;
-    }
-    f_head = n ? rel / n : 0;
-    f_chunk = rel - f_head * n;
+  // The copies' cursor: the next chunk to fetch, its item, chunk number there and context;
+  // this lane's group in it: table index and offset in the block.
+  int f_at = span_begin, f_seq = seq, f_head, f_chunk, f_ctx = context(seq), f_idx, f_off;
+  const int step_idx = CT / bs, step_off = CT - step_idx * bs;
+  auto place = [&]() {
     f_idx = (f_chunk * CT + c_sub * R) / bs;
     f_off = f_chunk * CT + c_sub * R - f_idx * bs;
+  };
+  {
+    const int rel = span_begin - seq_base, n = (f_ctx + CT - 1) / CT;
+    f_head = rel / n;
+    f_chunk = rel - f_head * n;
+    place();
   }
+  // on to the item of the cursor's chunk (which exists), if that is a later one
+  auto settle = [&]() {
+    if (f_chunk * CT < f_ctx) return false;
+    do {
+      f_chunk -= (f_ctx + CT - 1) / CT;
+      if (++f_head == Hkv) {
+        f_head = 0;
+        do {
+          f_ctx = context(++f_seq);
+        } while (f_ctx == 0);
+      }
+    } while (f_chunk * CT >= f_ctx);
+    place();
+    // its queries will be wanted in a moment
+    const char* q = reinterpret_cast<const char*>(a.q + ((size_t)f_seq * a.num_q_heads + f_head * G) * D);
+    if (lane * 128 < G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
+    return true;
+  };
   struct Group {
-    int blk, off, head;  // table entry, first token in the block (negative: nothing to copy), kv head
+    int chunk, blk, off, head;  // chunk (the span's end: none), table entry, first token in the block (negative:
+                                // nothing to copy), kv head
   };
   auto fetch = [&]() {
-    Group e{0, -1, f_head};
-    if (f_left > 0) {
+    Group e{span_end, 0, -1, 0};
+    if constexpr (TEAM) {
+      int c = 0;
+      if (lane == 0) c = atomicAdd(claims, 1);
+      c = __shfl_sync(0xffffffffu, c, 0);
+      if (c >= span_end) return e;
+      f_chunk += c - f_at;
+      f_at = c;
+      if (!settle()) place();
+    }
+    if (TEAM || f_at < span_end) {
+      e.chunk = f_at;
+      e.head = f_head;
       if (c_lane && f_chunk * CT + c_sub * R < f_ctx) {
         e.off = f_off;
         e.blk = __ldg(a.block_tables + (size_t)f_seq * a.max_blocks_per_seq + f_idx);
       }
-      f_chunk += team;
-      f_idx += step_idx;
-      f_off += step_off;
-      if (f_off >= bs) { f_off -= bs; ++f_idx; }
-      if (--f_left > 0 && f_chunk * CT >= f_ctx) {  // on to a later item, which exists
-        int n = (f_ctx + CT - 1) / CT;
-        do {
-          f_chunk -= n;
-          if (++f_head == Hkv) {
-            f_head = 0;
-            do {
-              f_ctx = context(++f_seq);
-            } while (f_ctx == 0);
-            n = (f_ctx + CT - 1) / CT;
-          }
-        } while (f_chunk >= n);
-        f_idx = (f_chunk * CT + c_sub * R) / bs;
-        f_off = f_chunk * CT + c_sub * R - f_idx * bs;
+      if (!TEAM && ++f_at < span_end) {
+        ++f_chunk;
+        f_idx += step_idx;
+        f_off += step_off;
+        if (f_off >= bs) { f_off -= bs; ++f_idx; }
+        settle();
       }
     }
     return e;
   };
-  auto issue = [&](int k, Group e) {
+  int ids[NST], issued = 0;  // chunks in flight
+  auto issue = [&](const Group& e) {
+    const int k = issued++;
+#pragma unroll
+    for (int i = 0; i < NST; ++i)
+      if (k % NST == i) ids[i] = e.chunk;
     const uint32_t bar = bar0 + (k % NST) * 8, dst = stage0 + (k % NST) * L::kStageBytes + c_dst;
     bool copy = e.off >= 0;
     if (copy && (unsigned)e.blk >= (unsigned)a.num_blocks) {  // rows outside the pool read as zeros
@@ -272,16 +285,6 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
     __syncwarp();
     if (copy) bulk_load(dst, c_base + ((long long)e.blk * Hkv + e.head) * run_bytes + e.off * c_unit, c_bytes, bar);
   };
-  {
-    Group e[NST];
-#pragma unroll
-    for (int k = 0; k < NST; ++k) e[k] = fetch();
-#pragma unroll
-    for (int k = 0; k < NST; ++k)
-      if (k < n_mine) issue(k, e[k]);
-  }
-  Group next = fetch();
-
   // ---- where a tile of 16 tokens lies in the stage: its rows 8 .. 15 are in a
   // group of their own when R is 8, two tiles share a group when R is 32
   constexpr int kCodeTile = R == 32 ? 16 * (D / 2) : 16 * L::kTokenBytes;
@@ -299,12 +302,19 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   const int v_sc = L::kPoolBytes + kScaleBase + t * (D / 16) + g * (D / 64) / 2;
 
   // ---- the items of the span, each from its chunk `first` to its end or the span's
-  int failed_at = n_mine;      // the chunk whose wait ran out
+  bool failed = false;         // a wait ran out
   int k = 0, at = span_begin;  // this warp's chunk count; the item's first chunk in the span
-  int ctx = context(seq), kvh = (span_begin - seq_base) / ((ctx + CT - 1) / CT);
-  int first = span_begin - seq_base - kvh * ((ctx + CT - 1) / CT);
+  int ctx = context(seq), kvh = f_head, first = f_chunk;
+  Group next = fetch();
   for (;;) {
     const int item_chunks = (ctx + CT - 1) / CT, len = min(item_chunks - first, span_end - at);
+    // what may be copied by now: a team's stages are free for its merge at the item's end
+    const int copy_end = TEAM ? at + len : span_end;
+    while (issued - k < NST && next.chunk < copy_end) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      issue(next);
+      next = fetch();
+    }
     const size_t head0 = (size_t)seq * a.num_q_heads + kvh * G;
 
     // queries as column fragments: thread (g, t) holds dims [t D/4, (t + 1) D/4) of heads g, g + 8
@@ -358,14 +368,22 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
       l[n][0] = l[n][1] = 0.f;
     }
 
-    for (; span_begin + rank + k * team < at + len; ++k) {
-      if (failed_at < n_mine) continue;
+    for (; k < issued; ++k) {
+      int chunk = ids[0];
+#pragma unroll
+      for (int i = 1; i < NST; ++i)
+        if (k % NST == i) chunk = ids[i];
+      if (chunk >= at + len) break;
+      if (failed) continue;
       if (!mbar_wait(bar0 + (k % NST) * 8, (k / NST) & 1, a.err)) {
-        failed_at = k;
+        // let the copies in flight land, and start no more
+        for (int i = k + 1; i < issued; ++i) mbar_wait(bar0 + (i % NST) * 8, (i / NST) & 1, a.err);
+        next.chunk = span_end;
+        failed = true;
         continue;
       }
       unsigned char* stage = stages + (k % NST) * L::kStageBytes;
-      const int n_valid = ctx - (first + span_begin + rank + k * team - at) * CT;  // of this chunk's tokens
+      const int n_valid = ctx - (first + chunk - at) * CT;  // of this chunk's tokens
       if (n_valid < CT) {
         // what lies behind the last token may be anything: codes are finite, V's scales need not be
         for (int tok = n_valid + lane; tok < CT; tok += 32) {
@@ -555,115 +573,227 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
       }
       __syncwarp();
       // the stage is free again: refill it
-      if (k + NST < n_mine) {
+      if (next.chunk < copy_end) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        issue(k + NST, next);
+        issue(next);
         next = fetch();
       }
     }
 
-    // ---- a team merges its warps: 2 and 3 into 0 and 1, then 1 into 0
-    bool failed = failed_at < n_mine;
-    if (!alone) {
-      float4* states = reinterpret_cast<float4*>(smem + L::kMerge) + lane;
-      constexpr int kSlot = L::kStateBytes / 16;
-      auto dump = [&](int slot) {
-        float4* to = states + slot * kSlot;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-            to[(n * (MT + 1) + i) * 32] = make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
-          to[(n * (MT + 1) + MT) * 32] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], d);
+        if (failed) l[n][j] = __int_as_float(0x7fc00000);
+      }
+
+    // From here a warp holds the rows i = row0, row0 + rows_step, ... of the
+    // state o[i][n] (all of them, or a team's warp every fourth) and every m and l.
+    const int row0 = TEAM ? warp : 0;
+    constexpr int rows_step = TEAM ? NW : 1, ROWS = (MT + rows_step - 1) / rows_step;
+    float4 x[ROWS][NT];
+    auto has = [&](int i) { return !TEAM || row0 + i * rows_step < MT; };
+    if constexpr (TEAM) {
+      float4* state = reinterpret_cast<float4*>(stages) + lane;  // every warp's, in its own stages
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          state[(n * (MT + 1) + i) * 32] = make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+        state[(n * (MT + 1) + MT) * 32] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float4* of[NW];
+        float4 ml[NW];
+        float w0[NW], w1[NW];
+        m[n][0] = m[n][1] = -1e30f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          of[w] = reinterpret_cast<const float4*>(smem + w * NST * L::kStageBytes) + lane + n * (MT + 1) * 32;
+          ml[w] = of[w][MT * 32];
+          m[n][0] = fmaxf(m[n][0], ml[w].x);
+          m[n][1] = fmaxf(m[n][1], ml[w].y);
         }
-      };
-      auto absorb = [&](int slot) {
-        const float4* from = states + slot * kSlot;
+        l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float4 s4 = from[(n * (MT + 1) + MT) * 32];
-          const float m0 = fmaxf(m[n][0], s4.x), m1 = fmaxf(m[n][1], s4.y);
-          const float a0 = ex2(m[n][0] - m0), a1 = ex2(m[n][1] - m1), b0 = ex2(s4.x - m0), b1 = ex2(s4.y - m1);
-          m[n][0] = m0;
-          m[n][1] = m1;
-          l[n][0] = l[n][0] * a0 + s4.z * b0;
-          l[n][1] = l[n][1] * a1 + s4.w * b1;
+        for (int w = 0; w < NW; ++w) {
+          w0[w] = ex2(ml[w].x - m[n][0]);
+          w1[w] = ex2(ml[w].y - m[n][1]);
+          l[n][0] = fmaf(ml[w].z, w0[w], l[n][0]);
+          l[n][1] = fmaf(ml[w].w, w1[w], l[n][1]);
+        }
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            const float4 v = from[(n * (MT + 1) + i) * 32];
-            o[i][n][0] = o[i][n][0] * a0 + v.x * b0;
-            o[i][n][1] = o[i][n][1] * a1 + v.y * b1;
-            o[i][n][2] = o[i][n][2] * a0 + v.z * b0;
-            o[i][n][3] = o[i][n][3] * a1 + v.w * b1;
+        for (int i = 0; i < ROWS; ++i) {
+          x[i][n] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!has(i)) continue;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const float4 v = of[w][(row0 + i * rows_step) * 32];
+            x[i][n].x = fmaf(v.x, w0[w], x[i][n].x);
+            x[i][n].y = fmaf(v.y, w1[w], x[i][n].y);
+            x[i][n].z = fmaf(v.z, w0[w], x[i][n].z);
+            x[i][n].w = fmaf(v.w, w1[w], x[i][n].w);
           }
         }
-      };
-      if (warp >= 2) dump(warp - 2);
-      failed = __syncthreads_or(failed);
-      if (warp < 2) absorb(warp);
-      if (warp == 1) dump(2);
-      __syncthreads();
-      if (warp == 0) absorb(2);
-    }
-    if (rank == 0) {
-      // an item within the span is finished; else a partial result: slot 2 i + 1 of
-      // worker i for an item that starts here, 2 i for one that started before
-      const bool direct = first == 0 && len == item_chunks;
-      const int slot = 2 * worker + (first == 0);
-      const float v_scale = __ldg(a.v_scale + kvh);
+      }
+    } else {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int h = kPairs ? 2 * (t & 1) + j : n * 8 + 2 * t + j;
-          float den = l[n][j];
+        for (int i = 0; i < ROWS; ++i) x[i][n] = make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+    }
+
+    // ---- an item cut by span borders: merge what has arrived
+    bool whole_item = first == 0 && len == item_chunks;
+    if (!whole_item) {
+      // chunk e lies in the span of worker ceil((e + 1) workers / chunks) - 1
+      const int item_at = at - first;  // the item's first chunk
+      const int lead = (int)(((long long)(item_at + 1) * workers - 1) / chunks);
+      const int parts = (int)(((long long)(item_at + item_chunks) * workers - 1) / chunks) - lead + 1;
+      constexpr int kState = Fp4State<D, GT>::kBytes / 16;
+      // part p: slot 2 i + 1 of worker i = lead for the item's first part, 2 i for those that started before span i
+      auto slot = [&](int p) { return partials + (size_t)(2 * (lead + p) + (p == 0)) * kState + lane; };
+      int node = worker - lead, width = 1;  // this result stands for the parts [node, node + width)
+      for (;;) {
+        float4* mine = slot(node);
 #pragma unroll
-          for (int d = 4; d <= 16; d <<= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
-          if (failed) den = __int_as_float(0x7fc00000);
-          float f = v_scale;
-          if (direct) f /= den;
-          // this thread's D / 8 dims of head h, two at a time
-          float v[D / 8];
-          if constexpr (kPairs) {
-            // threads t < 2 hold the even dims, t >= 2 the odd ones: each takes half of both
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              const float send = t < 2 ? o[i][0][j + 2] : o[i][0][j], keep = t < 2 ? o[i][0][j] : o[i][0][j + 2];
-              const float got = __shfl_xor_sync(0xffffffffu, send, 2);
-              v[2 * i] = (t < 2 ? keep : got) * f;  // pair 2i + (t >= 2) of the thread's D / 16
-              v[2 * i + 1] = (t < 2 ? got : keep) * f;
+          for (int i = 0; i < ROWS; ++i)
+            if (has(i)) __stcg(mine + (n * (MT + 1) + row0 + i * rows_step) * 32, x[i][n]);
+          if (row0 == 0) __stcg(mine + (n * (MT + 1) + MT) * 32, make_float4(m[n][0], m[n][1], l[n][0], l[n][1]));
+        }
+        // the node above: up to 8 children of this width, from part `up` on
+        int up, kids;
+        for (;;) {
+          up = node / (width * kFp4Radix) * (width * kFp4Radix);
+          kids = min(kFp4Radix, (parts - up + width - 1) / width);
+          if (kids > 1) break;
+          width *= kFp4Radix;  // an only child: nothing to merge at this level
+        }
+        __threadfence();
+        if constexpr (TEAM) __syncthreads();
+        else __syncwarp();
+        bool last = false;
+        if (TEAM ? threadIdx.x == 0 : lane == 0) {
+          // counted in the word of the second child's first span, under this call's tag
+          unsigned long long* word = arrivals + lead + up + width;
+          unsigned long long old = atomicAdd(word, 1ull);
+          if ((old & ~0xffull) != tag) {  // not opened yet: this call's first count replaces what was there
+            unsigned long long now = old + 1;
+            for (;;) {
+              const bool open = (now & ~0xffull) == tag;
+              old = atomicCAS(word, now, open ? now + 1 : tag | 1);
+              if (old == now) break;
+              now = old;
             }
-          } else {
+            if ((old & ~0xffull) != tag) old = tag;
+          }
+          last = (int)(old & 0xff) + 1 == kids;
+          if (last) __stcg(word, 0ull);  // for a replay of the same call
+          if constexpr (TEAM) claims[1] = last;
+        }
+        if constexpr (TEAM) {
+          __syncthreads();
+          last = *reinterpret_cast<volatile int*>(claims + 1) != 0;
+        } else {
+          last = __shfl_sync(0xffffffffu, (int)last, 0);
+        }
+        if (!last) break;
+        __threadfence();
+        // all children, in order, kBatch of them in flight
+        constexpr int kBatch = TEAM ? (GT == 16 ? 4 : 8) : GT == 4 ? 4 : GT == 8 ? 2 : 1;
+        for (int c0 = 0; c0 < kids; c0 += kBatch) {
+          float4 v[kBatch][NT][ROWS + 1];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              v[2 * i] = o[i][n][j] * f;
-              v[2 * i + 1] = o[i][n][j + 2] * f;
+          for (int b = 0; b < kBatch; ++b) {
+            const float4* from = slot(up + min(c0 + b, kids - 1) * width);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+              for (int i = 0; i < ROWS; ++i)
+                if (has(i)) v[b][n][i] = __ldcg(from + (n * (MT + 1) + row0 + i * rows_step) * 32);
+              v[b][n][ROWS] = __ldcg(from + (n * (MT + 1) + MT) * 32);
             }
           }
-          if (h >= G) continue;
-          const size_t row = direct ? head0 + h : (size_t)slot * G + h;
-          // pairs: v[2i], v[2i + 1] are dims 4i + 2 (t >> 1) and the next; else dims 2i and 2i + 1
-          const size_t dim0 = row * D + g * (D / 8) + (kPairs ? 2 * (t >> 1) : 0);
-          constexpr int kStep = kPairs ? 4 : 2;
-          if (direct) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-              *reinterpret_cast<uint32_t*>(a.out + dim0 + i * kStep) =
-                  (uint32_t)Elem<T>::from_f(v[2 * i]) | ((uint32_t)Elem<T>::from_f(v[2 * i + 1]) << 16);
-          } else {
+          for (int n = 0; n < NT; ++n) {
+            float m0 = c0 ? m[n][0] : -1e30f, m1 = c0 ? m[n][1] : -1e30f;
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-              *reinterpret_cast<float2*>(a.ws_acc + dim0 + i * kStep) = make_float2(v[2 * i], v[2 * i + 1]);
-            if (g == 0 && (!kPairs || t < 2)) *reinterpret_cast<float2*>(a.ws_ml + 2 * row) = make_float2(m[n][j], den);
+            for (int b = 0; b < kBatch; ++b) {
+              m0 = fmaxf(m0, v[b][n][ROWS].x);
+              m1 = fmaxf(m1, v[b][n][ROWS].y);
+            }
+            const float a0 = c0 ? ex2(m[n][0] - m0) : 0.f, a1 = c0 ? ex2(m[n][1] - m1) : 0.f;
+            m[n][0] = m0;
+            m[n][1] = m1;
+            l[n][0] = c0 ? l[n][0] * a0 : 0.f;
+            l[n][1] = c0 ? l[n][1] * a1 : 0.f;
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i)
+              x[i][n] = c0 ? make_float4(x[i][n].x * a0, x[i][n].y * a1, x[i][n].z * a0, x[i][n].w * a1)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+              if (c0 + b < kids) {
+                const float w0 = ex2(v[b][n][ROWS].x - m0), w1 = ex2(v[b][n][ROWS].y - m1);
+                l[n][0] = fmaf(v[b][n][ROWS].z, w0, l[n][0]);
+                l[n][1] = fmaf(v[b][n][ROWS].w, w1, l[n][1]);
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i)
+                  if (has(i)) {
+                    x[i][n].x = fmaf(v[b][n][i].x, w0, x[i][n].x);
+                    x[i][n].y = fmaf(v[b][n][i].y, w1, x[i][n].y);
+                    x[i][n].z = fmaf(v[b][n][i].z, w0, x[i][n].z);
+                    x[i][n].w = fmaf(v[b][n][i].w, w1, x[i][n].w);
+                  }
+              }
           }
         }
-      // the workers whose spans this item lies in: the merge reads their partials
-      if (first == 0 && lane == 0) {
-        // chunk e lies in the span of worker ceil((e + 1) workers / chunks) - 1
-        const int last = (int)(((long long)(at + item_chunks) * workers - 1) / chunks);
-        item_parts[(size_t)seq * Hkv + kvh] = make_int2(worker, last);
+        node = up;
+        width *= kFp4Radix;
+        if (width >= parts) {
+          whole_item = true;
+          break;
+        }
+        if constexpr (TEAM) __syncthreads();  // the children are read before the result takes the first one's slot
       }
     }
+
+    if (whole_item) {
+      const float v_scale = __ldg(a.v_scale + kvh);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float f[2] = {v_scale / l[n][0], v_scale / l[n][1]};
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+          if (!has(i)) continue;
+          const int row = row0 + i * rows_step;
+          const float y[2][2] = {{x[i][n].x * f[0], x[i][n].z * f[0]}, {x[i][n].y * f[1], x[i][n].w * f[1]}};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {  // columns 2t and 2t + 1
+            float v0 = y[j][0], v1 = y[j][1];
+            int h = n * 8 + 2 * t + j, dim = g * (D / 8) + 2 * row;
+            if constexpr (kPairs) {
+              // threads t < 2 hold the even dims of two pairs, t >= 2 the odd ones: each takes one pair
+              const float got = __shfl_xor_sync(0xffffffffu, t < 2 ? v1 : v0, 2);
+              if (t < 2) v1 = got;
+              else v0 = got;
+              h = 2 * (t & 1) + j;
+              dim = g * (D / 8) + 4 * row + 2 * (t >> 1);
+            }
+            if (h < G)
+              *reinterpret_cast<uint32_t*>(a.out + (head0 + h) * D + dim) =
+                  (uint32_t)Elem<T>::from_f(v0) | ((uint32_t)Elem<T>::from_f(v1) << 16);
+          }
+        }
+      }
+    }
+    if constexpr (TEAM) __syncthreads();  // the stages are free for copies again
     at += len;
     if (at >= span_end) break;
     first = 0;
@@ -674,138 +804,81 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
       } while (ctx == 0);
     }
   }
-  // after a failed wait let every copy in flight land before the CTA exits
-  for (int i = failed_at; i < min(n_mine, failed_at + NST); ++i)
-    mbar_wait(bar0 + (i % NST) * 8, (i / NST) & 1, a.err);
-}
-
-// Merge of the items that span borders cut: a CTA per (sequence, query head), warp w
-// the partials w, w + 4, ..., several loads in flight.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) decode_fp4_merge_kernel(const DecodeArgs a, const int2* item_parts) {
-  constexpr int VEC = D / 32, UN = 4;
-  __shared__ float sm[4][2 + D];
-  pdl_wait();  // every partial is written
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.group;
-  const int s = blockIdx.x / a.num_q_heads, h = blockIdx.x % a.num_q_heads;
-  if (__ldg(a.context_lens + s) <= 0 || a.max_context_len == 0) return;
-  const int2 parts = item_parts[(size_t)s * a.num_kv_heads + h / G];
-  if (parts.x == parts.y) return;  // written directly
-  float M = -INFINITY, den = 0.f, num[VEC] = {};
-  for (int p0 = parts.x + warp; p0 <= parts.y; p0 += 4 * UN) {
-    float2 ml[UN];
-    float v[UN][VEC], top = M;
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int p = min(p0 + 4 * u, parts.y);
-      const size_t r = (size_t)(2 * p + (p == parts.x)) * G + h % G;
-      ml[u] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * r);
-      if constexpr (VEC == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(a.ws_acc + r * D + lane * 4);
-        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(a.ws_acc + r * D + lane * 2);
-        v[u][0] = x.x; v[u][1] = x.y;
-      }
-      top = fmaxf(top, ml[u].x);
-    }
-    const float al = exp2f(M - top);
-    M = top;
-    den *= al;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) num[i] *= al;
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const float wt = p0 + 4 * u <= parts.y ? exp2f(ml[u].x - M) : 0.f;
-      den += ml[u].y * wt;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) num[i] += v[u][i] * wt;
-    }
-  }
-  if (lane == 0) {
-    sm[warp][0] = M;
-    sm[warp][1] = den;
-  }
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) sm[warp][2 + lane * VEC + i] = num[i];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    const float top = fmaxf(fmaxf(sm[0][0], sm[1][0]), fmaxf(sm[2][0], sm[3][0]));
-    float d = 0.f, n = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float wt = exp2f(sm[w][0] - top);  // 0 for a warp without partials
-      d += sm[w][1] * wt;
-      n += sm[w][2 + threadIdx.x] * wt;
-    }
-    a.out[(size_t)blockIdx.x * D + threadIdx.x] = Elem<T>::from_f(n / d);
-  }
 }
 
 namespace {
 
-template <typename T, int D, int GT, int R>
-cudaError_t launch_fp4(const DecodeArgs& a, const void* k, const void* v, const Fp4Split& w, int2* parts,
-                       cudaStream_t stream, int* launches) {
-  using L = Fp4Smem<D, GT>;
-  auto* kern = decode_fp4_kernel<T, D, GT, R>;
+struct Fp4Launch {
+  const unsigned char* k;
+  const unsigned char* v;
+  Fp4Split split;
+  float4* partials;
+  unsigned long long* arrivals;
+  cudaStream_t stream;
+};
+
+template <typename T, int D, int GT, int R, bool TEAM>
+cudaError_t launch_fp4(const DecodeArgs& a, const Fp4Launch& w) {
+  static_assert(Fp4State<D, GT>::kBytes <= kFp4Stages * Fp4Smem<D>::kStageBytes, "a team's warp merges from its stages");
+  auto* kern = decode_fp4_kernel<T, D, GT, R, TEAM>;
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = allow_smem(kern, L::kTotalMerge, &configured);
+  const cudaError_t e = allow_smem(kern, Fp4Smem<D>::kTotal, &configured);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3(w.ctas), dim3(kFp4Warps * 32), w.team == 1 ? L::kTotal : L::kTotalMerge, stream, a,
-                 static_cast<const unsigned char*>(k), static_cast<const unsigned char*>(v), w.workers, w.team, parts);
-  if (e == cudaSuccess) ++*launches;
-  if (e != cudaSuccess || w.workers == 1) return e;  // one span cuts no item
-  const long long rows = (long long)a.num_seqs * a.num_q_heads;
-  e = launch_pdl(decode_fp4_merge_kernel<T, D>, dim3((unsigned)rows), dim3(128), 0, stream, a,
-                 static_cast<const int2*>(parts));
-  if (e == cudaSuccess) ++*launches;
-  return e;
+  return launch_pdl(kern, dim3(w.split.ctas), dim3(kFp4Warps * 32), Fp4Smem<D>::kTotal, w.stream, a, w.k, w.v,
+                    w.split.workers, w.partials, w.arrivals);
+}
+
+template <typename T, int D, int GT, int R>
+cudaError_t launch_fp4_team(const DecodeArgs& a, const Fp4Launch& w) {
+  return w.split.team ? launch_fp4<T, D, GT, R, true>(a, w) : launch_fp4<T, D, GT, R, false>(a, w);
 }
 
 template <typename T, int D, int GT>
-cudaError_t launch_fp4_copy(const DecodeArgs& a, const void* k, const void* v, const Fp4Split& w, int2* parts,
-                            cudaStream_t st, int* n) {
+cudaError_t launch_fp4_copy(const DecodeArgs& a, const Fp4Launch& w) {
   // a copy's tokens lie in one block
-  if (a.block_size % 32 == 0) return launch_fp4<T, D, GT, 32>(a, k, v, w, parts, st, n);
-  if (a.block_size % 16 == 0) return launch_fp4<T, D, GT, 16>(a, k, v, w, parts, st, n);
-  return launch_fp4<T, D, GT, 8>(a, k, v, w, parts, st, n);
+  if (a.block_size % 32 == 0) return launch_fp4_team<T, D, GT, 32>(a, w);
+  if (a.block_size % 16 == 0) return launch_fp4_team<T, D, GT, 16>(a, w);
+  return launch_fp4_team<T, D, GT, 8>(a, w);
 }
 
 template <typename T, int D>
-cudaError_t launch_fp4_group(const DecodeArgs& a, const void* k, const void* v, const Fp4Split& w, int2* parts,
-                             cudaStream_t st, int* n) {
-  if (a.group <= 4) return launch_fp4_copy<T, D, 4>(a, k, v, w, parts, st, n);
-  if (a.group <= 8) return launch_fp4_copy<T, D, 8>(a, k, v, w, parts, st, n);
-  return launch_fp4_copy<T, D, 16>(a, k, v, w, parts, st, n);
+cudaError_t launch_fp4_group(const DecodeArgs& a, const Fp4Launch& w) {
+  if (a.group <= 4) return launch_fp4_copy<T, D, 4>(a, w);
+  if (a.group <= 8) return launch_fp4_copy<T, D, 8>(a, w);
+  return launch_fp4_copy<T, D, 16>(a, w);
+}
+
+template <typename T>
+cudaError_t launch_fp4_dim(const DecodeArgs& a, int head_dim, const Fp4Launch& w) {
+  return head_dim == 128 ? launch_fp4_group<T, 128>(a, w) : launch_fp4_group<T, 64>(a, w);
 }
 
 }  // namespace
 
 bool fp4_decode_split(int num_seqs, int num_kv_heads, int max_context_len, int partition_tokens, Fp4Split* w) {
-  *w = Fp4Split{1, 1, 1};
+  *w = Fp4Split{1, 1, false};
   if (num_seqs == 0) return true;
   if (max_context_len > 1 << 30) return false;
   const long long per_item = (max_context_len + kFp4Chunk - 1) / kFp4Chunk, items = (long long)num_seqs * num_kv_heads;
   if (items > 0x7fffffff || per_item * items > 0x7fffffffLL) return false;
   const int wave = 148 * kFp4Ctas;  // CTAs that a B200 holds at once
-  w->team = items >= FP4_TEAM ? 1 : kFp4Warps;
-  const long long least = (long long)w->team * (partition_tokens > 0 ? (partition_tokens + kFp4Chunk - 1) / kFp4Chunk : 1);
-  const long long most = (per_item * items + least - 1) / least;  // workers that have something to do
-  const long long all = (long long)wave * (kFp4Warps / w->team);
+  w->team = items < wave;
+  // a warp takes a chunk at least, or the caller's partition
+  const int least = (partition_tokens > 0 ? (partition_tokens + kFp4Chunk - 1) / kFp4Chunk : 1) * (w->team ? kFp4Warps : 1);
+  const long long most = (per_item * items + least - 1) / least, all = w->team ? wave : wave * kFp4Warps;
   w->workers = (int)(most < 1 ? 1 : most < all ? most : all);
   w->ctas = w->workers < wave ? w->workers : wave;
   return true;
 }
 
 cudaError_t launch_decode_fp4(const DecodeArgs& a, int dtype, int head_dim, const void* k_pool, const void* v_pool,
-                              const Fp4Split& split, int2* item_parts, cudaStream_t stream, int* launches) {
-  if (dtype == 0)
-    return head_dim == 128 ? launch_fp4_group<__half, 128>(a, k_pool, v_pool, split, item_parts, stream, launches)
-                           : launch_fp4_group<__half, 64>(a, k_pool, v_pool, split, item_parts, stream, launches);
-  return head_dim == 128 ? launch_fp4_group<__nv_bfloat16, 128>(a, k_pool, v_pool, split, item_parts, stream, launches)
-                         : launch_fp4_group<__nv_bfloat16, 64>(a, k_pool, v_pool, split, item_parts, stream, launches);
+                              const Fp4Split& split, void* partials, unsigned long long* arrivals, cudaStream_t stream,
+                              int* launches) {
+  const Fp4Launch w{static_cast<const unsigned char*>(k_pool), static_cast<const unsigned char*>(v_pool), split,
+                    static_cast<float4*>(partials), arrivals, stream};
+  const cudaError_t e = dtype == 0 ? launch_fp4_dim<__half>(a, head_dim, w) : launch_fp4_dim<__nv_bfloat16>(a, head_dim, w);
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 }  // namespace pa

@@ -173,13 +173,16 @@ cudaError_t launch_cache_gather(const GatherArgs& a, int dtype, int head_dim, in
                                 cudaStream_t stream, int* launches);
 
 // Attention over an E2M1 cache (pa_decode_fp4.cu): how a batch is split (false:
-// too many chunks).  a.ws_acc, a.ws_ml hold 2 * workers * group partial rows,
-// item_parts [num_seqs][Hkv] the workers an item is split over.
+// too many chunks).  `partials` holds 2 * workers states of fp4_state_bytes,
+// `arrivals` a word per worker (any contents: counts carry a.epoch as their tag).
 struct Fp4Split {
-  int ctas, workers, team;  // team: warps per worker
+  int ctas, workers;
+  bool team;  // a worker is a CTA (else a warp)
 };
 bool fp4_decode_split(int num_seqs, int num_kv_heads, int max_context_len, int partition_tokens, Fp4Split* split);
+int fp4_state_bytes(int head_dim, int group);
 cudaError_t launch_decode_fp4(const DecodeArgs& a, int dtype, int head_dim, const void* k_pool, const void* v_pool,
-                              const Fp4Split& split, int2* item_parts, cudaStream_t stream, int* launches);
+                              const Fp4Split& split, void* partials, unsigned long long* arrivals, cudaStream_t stream,
+                              int* launches);
 
 }  // namespace pa

@@ -72,14 +72,19 @@ def test_other_calls_refuse_an_fp4_cache(lib):
     assert lib.pa_cache_append_fp8(FAKE, FAKE, FAKE, 3, FAKE, FAKE, FAKE, FAKE, s, None) == INVALID
 
 
-def test_fp4_partitions_follow_the_work(lib):
-    """Default partitions are multiples of 128 up to 2048 and never need more workspace than 128-token ones."""
-    for seqs, maxlen in ((1, 1), (1, 1000), (6, 131071), (256, 4096), (64, 1024)):
+def test_fp4_workspace_follows_the_work(lib):
+    """Larger partitions never need more workspace, and no batch more than a full device's workers do."""
+    most = 0
+    for seqs, maxlen in ((1, 0), (1, 1), (1, 1000), (6, 131071), (64, 1024), (256, 4096), (4096, 4096)):
         s = pa.make_shape(num_seqs=seqs, num_q_heads=32, num_kv_heads=8, head_dim=128, block_size=16, num_blocks=64,
                           max_blocks_per_seq=8192, cache_format=pa.PA_CACHE_FP4_E2M1)
         auto = pa.pa_decode_workspace_bytes(s, maxlen)
-        s.partition_tokens = 128
-        assert 256 <= auto <= pa.pa_decode_workspace_bytes(s, maxlen)
+        most = max(most, auto)
+        for pt in (64, 128, 2048):
+            s.partition_tokens = pt
+            assert 0 < pa.pa_decode_workspace_bytes(s, maxlen) <= auto
+        assert pa.pa_decode_partition_tokens(s) == 2048
+    assert auto == most < 1 << 24
     assert pa.pa_decode_resolved_variant(s) == pa.PA_DECODE_TENSOR_CORES
 
 
