@@ -68,6 +68,15 @@ int effective_partition(const pa_shape* s) {
   return (s->shared_prefix || tensor_core_kernel(s, 512)) ? 512 : 1024;
 }
 
+// Bytes of one cached element (16-bit and E4M3 caches).
+int cache_elem_bytes(const pa_shape* s) { return s->cache_format == PA_CACHE_FP8_E4M3 ? 1 : 2; }
+
+// Bytes of one block of one pool: with an E2M1 cache 9 bytes per 16 elements.
+long long cache_block_bytes(const pa_shape* s) {
+  const long long elems = (long long)s->block_size * s->num_kv_heads * s->head_dim;
+  return s->cache_format == PA_CACHE_FP4_E2M1 ? elems / 16 * 9 : elems * cache_elem_bytes(s);
+}
+
 // Shape checks common to every call that touches the pool.
 pa_status check_pool_shape(const pa_shape* s) {
   if (!s) return PA_ERR_INVALID_ARG;
@@ -102,7 +111,7 @@ pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
   if (s->cache_format == PA_CACHE_FP4_E2M1) {
     if (s->variant != PA_DECODE_AUTO || s->shared_prefix) return PA_ERR_UNSUPPORTED;
     pa::Fp4Split split;
-    if (s->num_seqs > 0x7fffffff / s->num_q_heads) return PA_ERR_UNSUPPORTED;
+    if (s->num_seqs > 0x7fffffff / s->num_q_heads || cache_block_bytes(s) >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
     return pa::fp4_decode_split(s->num_seqs, s->num_kv_heads, max_context_len, s->partition_tokens, &split)
                ? PA_OK : PA_ERR_UNSUPPORTED;
   }
@@ -115,15 +124,6 @@ pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
   const long long parts = ((long long)max_context_len + pt - 1) / pt;
   if (512LL * s->num_kv_heads * (parts > 0 ? parts : 1) >= (1LL << 23)) return PA_ERR_UNSUPPORTED;
   return PA_OK;
-}
-
-// Bytes of one cached element (16-bit and E4M3 caches).
-int cache_elem_bytes(const pa_shape* s) { return s->cache_format == PA_CACHE_FP8_E4M3 ? 1 : 2; }
-
-// Bytes of one block of one pool: with an E2M1 cache 9 bytes per 16 elements.
-long long cache_block_bytes(const pa_shape* s) {
-  const long long elems = (long long)s->block_size * s->num_kv_heads * s->head_dim;
-  return s->cache_format == PA_CACHE_FP4_E2M1 ? elems / 16 * 9 : elems * cache_elem_bytes(s);
 }
 
 // Whether pa_decode runs the tensor-core variant for this (valid) shape.

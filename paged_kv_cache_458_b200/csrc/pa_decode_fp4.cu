@@ -72,12 +72,13 @@ struct Fp4Smem {
   static constexpr int kTotal = kTeam + 16;
 };
 
-// A warp's state as it is stored: GT columns of D dims (4 or 8 columns a tile), maxima and sums.
+// A warp's state as it is stored: output tiles, then maxima and sums.
 template <int D, int GT>
 struct Fp4State {
-  static constexpr int NT = GT == 16 ? 2 : 1;                // column tiles of 8
-  static constexpr int MT = GT == 4 ? D / 32 : D / 16;       // 16-row tiles of output dims, or of pairs of dims
-  static constexpr int kBytes = (MT + 1) * NT * 32 * 16;
+  static constexpr int NS = GT == 16 ? 2 : 1;            // tiles of 8 columns of logits
+  static constexpr int NV = GT == 4 ? 1 : 2;             // of outputs: with pairs of dims a column per head and parity
+  static constexpr int MT = GT == 16 ? D / 16 : D / 32;  // 16-row tiles of output dims, or of pairs of dims
+  static constexpr int kBytes = (MT * NV + NS) * 32 * 16;
 };
 int fp4_state_bytes(int head_dim, int group) {
   if (head_dim == 128) return group <= 4 ? Fp4State<128, 4>::kBytes : group <= 8 ? Fp4State<128, 8>::kBytes : Fp4State<128, 16>::kBytes;
@@ -119,8 +120,9 @@ __global__ void __launch_bounds__(kFp4Warps * 32, kFp4Ctas)
 decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
                   const unsigned char* __restrict__ v_pool, const int num_workers, float4* partials,
                   unsigned long long* arrivals) {
-  constexpr int NT = Fp4State<D, GT>::NT, MT = Fp4State<D, GT>::MT;
-  constexpr bool kPairs = GT == 4;      // V registers hold pairs of dims (see above), else pairs of tokens
+  constexpr int NS = Fp4State<D, GT>::NS, NV = Fp4State<D, GT>::NV, MT = Fp4State<D, GT>::MT;
+  constexpr bool kPairs = GT <= 8;  // V registers hold pairs of dims (see above), else pairs of tokens
+  constexpr bool kFolded = GT == 4;  // both dims of a pair in one column tile: even ones in columns 0 .. 3, odd in 4 .. 7
   using L = Fp4Smem<D>;
   constexpr bool kLo = std::is_same<T, __half>::value;  // p as hi + lo
   constexpr int NW = kFp4Warps, NST = kFp4Stages, CT = kFp4Chunk, TILES = 2;
@@ -199,16 +201,19 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   const bool c_lane = c_sub * R < CT && (c_piece == 0 || !whole);
   const uint32_t c_bytes = whole ? R * L::kTokenBytes : c_piece ? R * (D / 16) : R * (D / 2);
   const uint32_t c_dst = ((lane & 1) ? L::kPoolBytes : 0) + c_sub * R * L::kTokenBytes + (c_piece ? R * (D / 2) : 0);
-  const long long run_bytes = fp4_head_bytes(bs, D);
+  const int run_bytes = (int)fp4_head_bytes(bs, D);  // a block's bytes are below 2^31
+  const unsigned block_bytes = (unsigned)run_bytes * Hkv;
   const unsigned char* c_base = ((lane & 1) ? v_pool : k_pool) + (c_piece ? bs * (D / 2) : 0);
   const int c_unit = c_piece ? D / 16 : D / 2;
   // The copies' cursor: the next chunk to fetch, its item, chunk number there and context;
-  // this lane's group in it: table index and offset in the block.
-  int f_at = span_begin, f_seq = seq, f_head, f_chunk, f_ctx = context(seq), f_idx, f_off;
+  // this lane's group in it: its table entry and its offset in the block.
+  int f_at = span_begin, f_seq = seq, f_head, f_chunk, f_ctx = context(seq), f_off;
+  const int32_t* f_entry;          // of the group in the block table
   const int step_idx = CT / bs, step_off = CT - step_idx * bs;
   auto place = [&]() {
-    f_idx = (f_chunk * CT + c_sub * R) / bs;
-    f_off = f_chunk * CT + c_sub * R - f_idx * bs;
+    const int idx = (f_chunk * CT + c_sub * R) / bs;
+    f_off = f_chunk * CT + c_sub * R - idx * bs;
+    f_entry = a.block_tables + (size_t)f_seq * a.max_blocks_per_seq + idx;
   };
   {
     const int rel = span_begin - seq_base, n = (f_ctx + CT - 1) / CT;
@@ -254,13 +259,13 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
       e.head = f_head;
       if (c_lane && f_chunk * CT + c_sub * R < f_ctx) {
         e.off = f_off;
-        e.blk = __ldg(a.block_tables + (size_t)f_seq * a.max_blocks_per_seq + f_idx);
+        e.blk = __ldg(f_entry);
       }
       if (!TEAM && ++f_at < span_end) {
         ++f_chunk;
-        f_idx += step_idx;
+        f_entry += step_idx;
         f_off += step_off;
-        if (f_off >= bs) { f_off -= bs; ++f_idx; }
+        if (f_off >= bs) { f_off -= bs; ++f_entry; }
         settle();
       }
     }
@@ -283,7 +288,9 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
     const uint32_t total = __reduce_add_sync(0xffffffffu, copy ? c_bytes : 0u);
     if (lane == 0) mbar_arrive_expect_tx(bar, total);
     __syncwarp();
-    if (copy) bulk_load(dst, c_base + ((long long)e.blk * Hkv + e.head) * run_bytes + e.off * c_unit, c_bytes, bar);
+    if (copy)
+      bulk_load(dst, c_base + (unsigned long long)(unsigned)e.blk * block_bytes + (unsigned)(e.head * run_bytes + e.off * c_unit),
+                c_bytes, bar);
   };
   // ---- where a tile of 16 tokens lies in the stage: its rows 8 .. 15 are in a
   // group of their own when R is 8, two tiles share a group when R is 32
@@ -318,12 +325,13 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
     const size_t head0 = (size_t)seq * a.num_q_heads + kvh * G;
 
     // queries as column fragments: thread (g, t) holds dims [t D/4, (t + 1) D/4) of heads g, g + 8
+    // The logit scale is kept positive: its sign goes into the queries, and a zero scale zeroes them.
     const float cscale = a.scale_log2 * __ldg(a.k_scale + kvh);
-    uint32_t bq[NT][KW * 4];
-    float xs[NT][2];  // logit scale of this thread's columns 2t, 2t + 1
+    uint32_t bq[NS][KW * 4];
+    float xs[NS][2];  // logit scale of this thread's columns 2t, 2t + 1
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int h = kPairs ? g & 3 : n * 8 + g;  // pairs: columns 4 .. 7 repeat the heads
+    for (int n = 0; n < NS; ++n) {
+      const int h = kFolded ? g & 3 : n * 8 + g;  // folded: columns 4 .. 7 repeat the heads
       uint32_t w[KW * 4];
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
@@ -331,11 +339,8 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
         if (h < G) v = *reinterpret_cast<const uint4*>(a.q + (head0 + h) * D + t * (D / 4) + i * 8);
         w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
       }
-      if constexpr (kLo) {
-#pragma unroll
-        for (int i = 0; i < KW * 4; ++i) bq[n][i] = w[i];
-        xs[n][0] = xs[n][1] = cscale;
-      } else {
+      float down = 1.f;
+      if constexpr (!kLo) {
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < KW * 4; ++i) {
@@ -346,24 +351,31 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = max((int)(__float_as_uint(top) >> 23), 15);  // 2^(e - 127) <= top
         const float up = __uint_as_float((uint32_t)(268 - e) << 23);  // 2^(141 - e)
-        const float down = __uint_as_float((uint32_t)(e - 14) << 23);
+        down = __uint_as_float((uint32_t)(e - 14) << 23);
 #pragma unroll
         for (int i = 0; i < KW * 4; ++i) {
           const float2 f = Elem<T>::to_f2(w[i]);
-          bq[n][i] = f16x2_of(f.x * up, f.y * up);
+          w[i] = f16x2_of(f.x * up, f.y * up);
         }
-        xs[n][0] = cscale * __shfl_sync(0xffffffffu, down, 8 * t);
-        xs[n][1] = cscale * __shfl_sync(0xffffffffu, down, 8 * t + 4);
       }
+      const float c = cscale * down;
+#pragma unroll
+      for (int i = 0; i < KW * 4; ++i) bq[n][i] = c == 0.f ? 0u : c < 0.f ? w[i] ^ 0x80008000u : w[i];
+      const float pos = c == 0.f ? 1.f : fabsf(c);
+      xs[n][0] = __shfl_sync(0xffffffffu, pos, 8 * t);
+      xs[n][1] = __shfl_sync(0xffffffffu, pos, 8 * t + 4);
     }
 
-    float o[MT][NT][4], m[NT][2], l[NT][2];
+    float o[MT][NV][4], m[NS][2], l[NS][2];
+    constexpr auto tile_of = [](int v) { return GT == 16 ? v : 0; };  // the logits' tile of an output tile
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][n][j] = 0.f;
+        for (int j = 0; j < 4; ++j) o[i][v][j] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
       m[n][0] = m[n][1] = -1e30f;
       l[n][0] = l[n][1] = 0.f;
     }
@@ -398,7 +410,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
         const unsigned char* st = stage + half * L::kTokenBytes;
 
         // ---- logits
-        float x[TILES][NT][4];
+        float x[TILES][NS][4];
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
           uint32_t ca[KW], cb[KW], sa, sb;
@@ -430,7 +442,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
               fb[j] = hmul2(fb[j], db);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NS; ++n) {
               if (w == 0) mma_f16_first(x[i][n], fa[0], fb[0], fa[1], fb[1], bq[n][0], bq[n][1]);
               else mma_f16(x[i][n], fa[0], fb[0], fa[1], fb[1], bq[n][4 * w], bq[n][4 * w + 1]);
               mma_f16(x[i][n], fa[2], fb[2], fa[3], fb[3], bq[n][4 * w + 2], bq[n][4 * w + 3]);
@@ -440,16 +452,10 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 
         // ---- softmax
         bool grow = false;
-        float top[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < TILES; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[i][n][j] *= xs[n][j & 1];
+        float top[NS][2];
         if (half + 32 > n_valid) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < TILES; ++i)
 #pragma unroll
@@ -458,14 +464,14 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
           __syncwarp();
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          top[n][0] = fmaxf(fmaxf(x[0][n][0], x[0][n][2]), fmaxf(x[1][n][0], x[1][n][2]));
-          top[n][1] = fmaxf(fmaxf(x[0][n][1], x[0][n][3]), fmaxf(x[1][n][1], x[1][n][3]));
+        for (int n = 0; n < NS; ++n) {
+          top[n][0] = xs[n][0] * fmaxf(fmaxf(x[0][n][0], x[0][n][2]), fmaxf(x[1][n][0], x[1][n][2]));
+          top[n][1] = xs[n][1] * fmaxf(fmaxf(x[0][n][1], x[0][n][3]), fmaxf(x[1][n][1], x[1][n][3]));
           grow |= top[n][0] > m[n][0] + 8.f || top[n][1] > m[n][1] + 8.f;
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               float v = top[n][j];
@@ -475,22 +481,26 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
               m[n][j] = mn;
               l[n][j] *= al;
 #pragma unroll
-              for (int i = 0; i < MT; ++i) {
-                o[i][n][j] *= al;
-                o[i][n][j + 2] *= al;
-              }
+              for (int w = 0; w < NV; ++w)
+                if (tile_of(w) == n) {
+#pragma unroll
+                  for (int i = 0; i < MT; ++i) {
+                    o[i][w][j] *= al;
+                    o[i][w][j + 2] *= al;
+                  }
+                }
             }
         }
 
         // ---- probabilities as column fragments, and O^T += V^T P^T
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
-          uint32_t hi[NT][2], lo[NT][2];
+          uint32_t hi[NS][2], lo[NS][2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float p0 = ex2(x[i][n][2 * j] - m[n][0]), p1 = ex2(x[i][n][2 * j + 1] - m[n][1]);
+              const float p0 = ex2(fmaf(x[i][n][2 * j], xs[n][0], -m[n][0])), p1 = ex2(fmaf(x[i][n][2 * j + 1], xs[n][1], -m[n][1]));
               l[n][0] += p0;
               l[n][1] += p1;
               const uint32_t h = f16x2_of(p0, p1);
@@ -520,11 +530,16 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 #pragma unroll
             for (int r = 0; r < 2; ++r) {  // 8 tokens a product: t and t + 4, then t + 8 and t + 12
               const uint32_t s0 = __byte_perm(sc[r], 0, 0x1010), s1 = __byte_perm(sc[r], 0, 0x3232);
-              const uint32_t b0 = __byte_perm(hi[0][r], 0, pair_lo), b1 = __byte_perm(hi[0][r], 0, pair_hi);
-              uint32_t d0 = 0, d1 = 0;
-              if constexpr (kLo) {
-                d0 = __byte_perm(lo[0][r], 0, pair_lo);
-                d1 = __byte_perm(lo[0][r], 0, pair_hi);
+              uint32_t b0[NV], b1[NV], d0[NV], d1[NV];
+#pragma unroll
+              for (int v = 0; v < NV; ++v) {
+                const uint32_t at_lo = kFolded ? pair_lo : v ? 0x1044 : 0x4410, at_hi = kFolded ? pair_hi : v ? 0x3244 : 0x4432;
+                b0[v] = __byte_perm(hi[0][r], 0, at_lo);
+                b1[v] = __byte_perm(hi[0][r], 0, at_hi);
+                if constexpr (kLo) {
+                  d0[v] = __byte_perm(lo[0][r], 0, at_lo);
+                  d1[v] = __byte_perm(lo[0][r], 0, at_hi);
+                }
               }
 #pragma unroll
               for (int w = 0; w < VW; ++w) {
@@ -537,11 +552,13 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
                   f1[j] = hmul2(f1[j], s1);
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  mma_f16(o[2 * w + j][0], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], b0, b1);
-                  if constexpr (kLo)
-                    mma_f16(o[2 * w + j][0], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], d0, d1);
-                }
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                  for (int v = 0; v < NV; ++v) {
+                    mma_f16(o[2 * w + j][v], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], b0[v], b1[v]);
+                    if constexpr (kLo)
+                      mma_f16(o[2 * w + j][v], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], d0[v], d1[v]);
+                  }
               }
             }
           } else {
@@ -562,7 +579,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < NS; ++n) {
                   mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], hi[n][0], hi[n][1]);
                   if constexpr (kLo)
                     mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], lo[n][0], lo[n][1]);
@@ -581,7 +598,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
     }
 
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -590,61 +607,66 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
       }
 
     // From here a warp holds the rows i = row0, row0 + rows_step, ... of the
-    // state o[i][n] (all of them, or a team's warp every fourth) and every m and l.
+    // state o[i][v] (all of them, or a team's warp every fourth) and every m and l.
     const int row0 = TEAM ? warp : 0;
     constexpr int rows_step = TEAM ? NW : 1, ROWS = (MT + rows_step - 1) / rows_step;
-    float4 x[ROWS][NT];
+    float4 x[ROWS][NV];
     auto has = [&](int i) { return !TEAM || row0 + i * rows_step < MT; };
+    auto at_row = [&](int i, int v) { return (v * MT + row0 + i * rows_step) * 32; };  // in a stored state
+    auto at_ml = [&](int n) { return (MT * NV + n) * 32; };
+    // adds w0, w1 (columns 2t, 2t + 1) times a stored state's rows
+    auto add = [](float4& to, const float4& v, float w0, float w1) {
+      to.x = fmaf(v.x, w0, to.x);
+      to.y = fmaf(v.y, w1, to.y);
+      to.z = fmaf(v.z, w0, to.z);
+      to.w = fmaf(v.w, w1, to.w);
+    };
     if constexpr (TEAM) {
       float4* state = reinterpret_cast<float4*>(stages) + lane;  // every warp's, in its own stages
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-          state[(n * (MT + 1) + i) * 32] = make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
-        state[(n * (MT + 1) + MT) * 32] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
-      }
+        for (int i = 0; i < MT; ++i) state[(v * MT + i) * 32] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
+#pragma unroll
+      for (int n = 0; n < NS; ++n) state[at_ml(n)] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
       __syncthreads();
+      const float4* of[NW];
+      float w0[NS][NW], w1[NS][NW];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float4* of[NW];
+      for (int w = 0; w < NW; ++w) of[w] = reinterpret_cast<const float4*>(smem + w * NST * L::kStageBytes) + lane;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
         float4 ml[NW];
-        float w0[NW], w1[NW];
         m[n][0] = m[n][1] = -1e30f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-          of[w] = reinterpret_cast<const float4*>(smem + w * NST * L::kStageBytes) + lane + n * (MT + 1) * 32;
-          ml[w] = of[w][MT * 32];
+          ml[w] = of[w][at_ml(n)];
           m[n][0] = fmaxf(m[n][0], ml[w].x);
           m[n][1] = fmaxf(m[n][1], ml[w].y);
         }
         l[n][0] = l[n][1] = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-          w0[w] = ex2(ml[w].x - m[n][0]);
-          w1[w] = ex2(ml[w].y - m[n][1]);
-          l[n][0] = fmaf(ml[w].z, w0[w], l[n][0]);
-          l[n][1] = fmaf(ml[w].w, w1[w], l[n][1]);
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          x[i][n] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!has(i)) continue;
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const float4 v = of[w][(row0 + i * rows_step) * 32];
-            x[i][n].x = fmaf(v.x, w0[w], x[i][n].x);
-            x[i][n].y = fmaf(v.y, w1[w], x[i][n].y);
-            x[i][n].z = fmaf(v.z, w0[w], x[i][n].z);
-            x[i][n].w = fmaf(v.w, w1[w], x[i][n].w);
-          }
+          w0[n][w] = ex2(ml[w].x - m[n][0]);
+          w1[n][w] = ex2(ml[w].y - m[n][1]);
+          l[n][0] = fmaf(ml[w].z, w0[n][w], l[n][0]);
+          l[n][1] = fmaf(ml[w].w, w1[n][w], l[n][1]);
         }
       }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          x[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!has(i)) continue;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) add(x[i][v], of[w][at_row(i, v)], w0[tile_of(v)][w], w1[tile_of(v)][w]);
+        }
     } else {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) x[i][n] = make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+        for (int i = 0; i < ROWS; ++i) x[i][v] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
     }
 
     // ---- an item cut by span borders: merge what has arrived
@@ -661,11 +683,13 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
       for (;;) {
         float4* mine = slot(node);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int i = 0; i < ROWS; ++i)
-            if (has(i)) __stcg(mine + (n * (MT + 1) + row0 + i * rows_step) * 32, x[i][n]);
-          if (row0 == 0) __stcg(mine + (n * (MT + 1) + MT) * 32, make_float4(m[n][0], m[n][1], l[n][0], l[n][1]));
+            if (has(i)) __stcg(mine + at_row(i, v), x[i][v]);
+        if (row0 == 0) {
+#pragma unroll
+          for (int n = 0; n < NS; ++n) __stcg(mine + at_ml(n), make_float4(m[n][0], m[n][1], l[n][0], l[n][1]));
         }
         // the node above: up to 8 children of this width, from part `up` on
         int up, kids;
@@ -708,51 +732,59 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
         // all children, in order, kBatch of them in flight
         constexpr int kBatch = TEAM ? (GT == 16 ? 4 : 8) : GT == 4 ? 4 : GT == 8 ? 2 : 1;
         for (int c0 = 0; c0 < kids; c0 += kBatch) {
-          float4 v[kBatch][NT][ROWS + 1];
+          float4 y[kBatch][ROWS][NV], ml[kBatch][NS];
 #pragma unroll
           for (int b = 0; b < kBatch; ++b) {
             const float4* from = slot(up + min(c0 + b, kids - 1) * width);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NS; ++n) ml[b][n] = __ldcg(from + at_ml(n));
 #pragma unroll
-              for (int i = 0; i < ROWS; ++i)
-                if (has(i)) v[b][n][i] = __ldcg(from + (n * (MT + 1) + row0 + i * rows_step) * 32);
-              v[b][n][ROWS] = __ldcg(from + (n * (MT + 1) + MT) * 32);
-            }
+            for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+              for (int v = 0; v < NV; ++v)
+                if (has(i)) y[b][i][v] = __ldcg(from + at_row(i, v));
           }
+          float a0[NS], a1[NS];  // weights of what has been added up so far
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NS; ++n) {
             float m0 = c0 ? m[n][0] : -1e30f, m1 = c0 ? m[n][1] : -1e30f;
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-              m0 = fmaxf(m0, v[b][n][ROWS].x);
-              m1 = fmaxf(m1, v[b][n][ROWS].y);
+              m0 = fmaxf(m0, ml[b][n].x);
+              m1 = fmaxf(m1, ml[b][n].y);
             }
-            const float a0 = c0 ? ex2(m[n][0] - m0) : 0.f, a1 = c0 ? ex2(m[n][1] - m1) : 0.f;
+            a0[n] = ex2(m[n][0] - m0);
+            a1[n] = ex2(m[n][1] - m1);
             m[n][0] = m0;
             m[n][1] = m1;
-            l[n][0] = c0 ? l[n][0] * a0 : 0.f;
-            l[n][1] = c0 ? l[n][1] * a1 : 0.f;
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i)
-              x[i][n] = c0 ? make_float4(x[i][n].x * a0, x[i][n].y * a1, x[i][n].z * a0, x[i][n].w * a1)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-              if (c0 + b < kids) {
-                const float w0 = ex2(v[b][n][ROWS].x - m0), w1 = ex2(v[b][n][ROWS].y - m1);
-                l[n][0] = fmaf(v[b][n][ROWS].z, w0, l[n][0]);
-                l[n][1] = fmaf(v[b][n][ROWS].w, w1, l[n][1]);
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i)
-                  if (has(i)) {
-                    x[i][n].x = fmaf(v[b][n][i].x, w0, x[i][n].x);
-                    x[i][n].y = fmaf(v[b][n][i].y, w1, x[i][n].y);
-                    x[i][n].z = fmaf(v[b][n][i].z, w0, x[i][n].z);
-                    x[i][n].w = fmaf(v[b][n][i].w, w1, x[i][n].w);
-                  }
-              }
+            l[n][0] = c0 ? l[n][0] * a0[n] : 0.f;
+            l[n][1] = c0 ? l[n][1] * a1[n] : 0.f;
           }
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              const float w0 = a0[tile_of(v)], w1 = a1[tile_of(v)];
+              x[i][v] = c0 ? make_float4(x[i][v].x * w0, x[i][v].y * w1, x[i][v].z * w0, x[i][v].w * w1)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+            if (c0 + b < kids) {
+              float w0[NS], w1[NS];
+#pragma unroll
+              for (int n = 0; n < NS; ++n) {
+                w0[n] = ex2(ml[b][n].x - m[n][0]);
+                w1[n] = ex2(ml[b][n].y - m[n][1]);
+                l[n][0] = fmaf(ml[b][n].z, w0[n], l[n][0]);
+                l[n][1] = fmaf(ml[b][n].w, w1[n], l[n][1]);
+              }
+#pragma unroll
+              for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                  if (has(i)) add(x[i][v], y[b][i][v], w0[tile_of(v)], w1[tile_of(v)]);
+            }
         }
         node = up;
         width *= kFp4Radix;
@@ -766,29 +798,40 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 
     if (whole_item) {
       const float v_scale = __ldg(a.v_scale + kvh);
+      auto pair = [](float v0, float v1) {
+        return (uint32_t)Elem<T>::from_f(v0) | ((uint32_t)Elem<T>::from_f(v1) << 16);
+      };
+      uint16_t* out = a.out + head0 * D + g * (D / 8);  // this thread's dims of head 0
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float f[2] = {v_scale / l[n][0], v_scale / l[n][1]};
+      for (int i = 0; i < ROWS; ++i) {
+        if (!has(i)) continue;
+        const int row = row0 + i * rows_step;
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          if (!has(i)) continue;
-          const int row = row0 + i * rows_step;
-          const float y[2][2] = {{x[i][n].x * f[0], x[i][n].z * f[0]}, {x[i][n].y * f[1], x[i][n].w * f[1]}};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {  // columns 2t and 2t + 1
-            float v0 = y[j][0], v1 = y[j][1];
-            int h = n * 8 + 2 * t + j, dim = g * (D / 8) + 2 * row;
-            if constexpr (kPairs) {
-              // threads t < 2 hold the even dims of two pairs, t >= 2 the odd ones: each takes one pair
-              const float got = __shfl_xor_sync(0xffffffffu, t < 2 ? v1 : v0, 2);
-              if (t < 2) v1 = got;
-              else v0 = got;
-              h = 2 * (t & 1) + j;
-              dim = g * (D / 8) + 4 * row + 2 * (t >> 1);
-            }
+        for (int j = 0; j < 2; ++j) {  // columns 2t and 2t + 1
+          auto first_of = [&](int v) { return j ? x[i][v].y : x[i][v].x; };    // of the tile's row g
+          auto second_of = [&](int v) { return j ? x[i][v].w : x[i][v].z; };  // of row g + 8
+          if constexpr (kFolded) {
+            // threads t < 2 hold the even dims of two pairs, t >= 2 the odd ones: each takes one pair
+            const float f = v_scale / l[0][j];
+            float v0 = first_of(0) * f, v1 = second_of(0) * f;
+            const float got = __shfl_xor_sync(0xffffffffu, t < 2 ? v1 : v0, 2);
+            if (t < 2) v1 = got;
+            else v0 = got;
+            const int h = 2 * (t & 1) + j;
+            if (h < G) *reinterpret_cast<uint32_t*>(out + h * D + 4 * row + 2 * (t >> 1)) = pair(v0, v1);
+          } else if constexpr (kPairs) {
+            const float f = v_scale / l[0][j];
+            const int h = 2 * t + j;
             if (h < G)
-              *reinterpret_cast<uint32_t*>(a.out + (head0 + h) * D + dim) =
-                  (uint32_t)Elem<T>::from_f(v0) | ((uint32_t)Elem<T>::from_f(v1) << 16);
+              *reinterpret_cast<uint2*>(out + h * D + 4 * row) =
+                  make_uint2(pair(first_of(0) * f, first_of(1) * f), pair(second_of(0) * f, second_of(1) * f));
+          } else {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              const float f = v_scale / l[tile_of(v)][j];
+              const int h = v * 8 + 2 * t + j;
+              if (h < G) *reinterpret_cast<uint32_t*>(out + h * D + 2 * row) = pair(first_of(v) * f, second_of(v) * f);
+            }
           }
         }
       }
