@@ -69,18 +69,22 @@ __device__ __forceinline__ float div_by(float x, float h, float y) {
   return fabsf(r) > 0.f ? __fmaf_rn(r, y, q) : q;
 }
 
-// Largest magnitude of 8 packed elements, NaN if one is NaN.
+// The larger magnitude of two pairs of packed elements, NaN if one is NaN; the signs come out mixed.
 template <typename T>
-__device__ __forceinline__ float amax8(const uint32_t (&w)[4]) {
-  auto top = [](uint32_t a, uint32_t b) {
-    uint32_t r;
-    if constexpr (std::is_same<T, __half>::value) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-  };
-  constexpr uint32_t kAbs = 0x7fff7fffu;
-  const uint32_t m = top(top(w[0] & kAbs, w[1] & kAbs), top(w[2] & kAbs, w[3] & kAbs));
-  return Elem<T>::to_f2(top(m, __byte_perm(m, 0, 0x1032))).x;
+__device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (std::is_same<T, __half>::value) asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t top8(const uint32_t (&w)[4]) {
+  return top2<T>(top2<T>(w[0], w[1]), top2<T>(w[2], w[3]));
+}
+// The largest magnitude in a pair.
+template <typename T>
+__device__ __forceinline__ float magnitude(uint32_t pair) {
+  return Elem<T>::to_f2(top2<T>(pair, __byte_perm(pair, 0, 0x1032)) & 0x7fffu).x;
 }
 
 // A kv head's scale, its reciprocal, and whether that and the products with it stay well inside fp32's range.
@@ -104,7 +108,7 @@ __device__ __forceinline__ uint2 e4m3x8_of(const uint32_t (&w)[4], const HeadSca
   }
   // a quotient beyond fp32 (a bf16 row) must come out infinite, not NaN; fp16's are below 2^77
   bool safe = s.safe;
-  if (!std::is_same<T, __half>::value) safe = safe && !(amax8<T>(w) * s.y >= 0x1p100f);
+  if (!std::is_same<T, __half>::value) safe = safe && !(magnitude<T>(top8<T>(w)) * s.y >= 0x1p100f);
   if (safe) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = div_by(f[j], s.h, s.y);
@@ -159,7 +163,8 @@ __device__ __forceinline__ uint32_t e2m1x8_of(const uint32_t (&w)[4], float r) {
 constexpr int kRowWarps = 4, kRowStages = 3, kRowCtas = 4;
 constexpr int kTaskBytes = 4096, kStageBytes = kTaskBytes + 512;  // rows, then the table's row
 
-template <typename T, int FMT, int D>
+// ROT: whether anything rotates.
+template <typename T, int FMT, int D, bool ROT>
 __global__ void __launch_bounds__(kRowWarps * 32, kRowCtas)
 rope_append_kernel(const RopeArgs a, const int num_tokens, const FastDiv by_block) {
   constexpr int LANES = D / 16, RW = 32 / LANES;   // lanes per row, rows per step
@@ -199,14 +204,14 @@ rope_append_kernel(const RopeArgs a, const int num_tokens, const FastDiv by_bloc
   // skipped; what is wrong with a token is reported with its first task.
   auto issue = [&](int slot, int pos) {
     const bool padding = slot < 0, bad_slot = slot >= num_slots;
-    const bool bad_pos = a.rotary_dim > 0 && (unsigned)pos >= (unsigned)a.max_position;
+    const bool bad_pos = ROT && (unsigned)pos >= (unsigned)a.max_position;
     if (padding || bad_slot || bad_pos) {
       if (!padding && f_part == 0 && lane == 0) report(a.err, bad_slot ? kErrSlot : kErrPosition);
       slot = -1;
     }
     const bool is_q = f_part < q_tasks;
     const uint32_t bytes = slot < 0 ? 0 : heads_of(f_part) * D * 2;
-    const uint32_t table_bytes = slot < 0 ? 0 : a.rotary_dim * 4;
+    const uint32_t table_bytes = !ROT || slot < 0 ? 0 : a.rotary_dim * 4;
     if (lane == 0) {
       const uint32_t bar = bar0 + f_stage * 8, dst = smem_addr(stages + f_stage * kStageBytes);
       const int from = head_of(f_part) * D;
@@ -226,7 +231,7 @@ rope_append_kernel(const RopeArgs a, const int num_tokens, const FastDiv by_bloc
     return slot;
   };
   auto slot_of = [&](int t) { return __ldg(a.slot_mapping + t); };
-  auto pos_of = [&](int t) { return a.rotary_dim > 0 ? __ldg(a.positions + t) : 0; };
+  auto pos_of = [&](int t) { return ROT ? __ldg(a.positions + t) : 0; };
   int t = f_t, part = f_part, stage_at = 0, phase = 0;  // the task at work
 #pragma unroll
   for (int k = 0; k < kRowStages; ++k) slots[k] = k < n_mine ? issue(slot_of(f_t), pos_of(f_t)) : -1;
@@ -252,8 +257,8 @@ rope_append_kernel(const RopeArgs a, const int num_tokens, const FastDiv by_bloc
 #pragma unroll 1
       for (int is_v = 0; is_v < (is_q ? 1 : 2); ++is_v) {
         // this lane's two units: a unit and its partner (half pairing), else neighbours
-        const int hu = is_v || a.interleaved ? 0 : a.rotary_dim / 16;  // units per half
-        const bool split = p < hu, turn = split || (!is_v && a.interleaved && p * 16 < a.rotary_dim);
+        const int hu = !ROT || is_v || a.interleaved ? 0 : a.rotary_dim / 16;  // units per half
+        const bool split = p < hu, turn = split || (ROT && !is_v && a.interleaved && p * 16 < a.rotary_dim);
         const int u0 = split ? p : hu + p + (p - hu), u1 = split ? p + hu : u0 + 1;
         // half pairing: cos and sin of the pairs (unit, partner); interleaved: of the 4 pairs of u0, then of u1
         alignas(16) float cs[8], sn[8];
@@ -329,12 +334,11 @@ rope_append_kernel(const RopeArgs a, const int num_tokens, const FastDiv by_bloc
             }
           } else if constexpr (FMT == kFmtFp4) {
             const HeadScale s = head_scale(live ? __ldg(scale) : 1.f);
-            const float m0 = amax8<T>(w0), m1 = amax8<T>(w1);
+            const uint32_t m0 = top8<T>(w0), m1 = top8<T>(w1);
             uint32_t* codes = reinterpret_cast<uint32_t*>(to);
-            auto larger = [](float x, float y) { return x != x ? x : y != y ? y : fmaxf(x, y); };
             if (hu == 0) {  // neighbours: one block
               float f;
-              const uint8_t sc = block_scale(larger(m0, m1), s, &f);
+              const uint8_t sc = block_scale(magnitude<T>(top2<T>(m0, m1)), s, &f);
               const uint32_t o0 = e2m1x8_of<T>(w0, f), o1 = e2m1x8_of<T>(w1, f);
               if (live) {
                 *reinterpret_cast<uint2*>(codes + u0) = make_uint2(o0, o1);
@@ -345,12 +349,13 @@ rope_append_kernel(const RopeArgs a, const int num_tokens, const FastDiv by_bloc
               auto mate = [&](int u) {
                 const int v = u ^ 1, l = v < hu ? v : v < 2 * hu ? v - hu : hu + (v - 2 * hu) / 2;
                 const int src = lane - p + l;
-                const float f0 = __shfl_sync(0xffffffffu, m0, src), f1 = __shfl_sync(0xffffffffu, m1, src);
+                const uint32_t f0 = __shfl_sync(0xffffffffu, m0, src), f1 = __shfl_sync(0xffffffffu, m1, src);
                 return v < hu || (v >= 2 * hu && (v & 1) == 0) ? f0 : f1;
               };
-              const float n0 = mate(u0), n1 = mate(u1);
+              const uint32_t n0 = mate(u0), n1 = mate(u1);
               float f0, f1;
-              const uint8_t s0 = block_scale(larger(m0, n0), s, &f0), s1 = block_scale(larger(m1, n1), s, &f1);
+              const uint8_t s0 = block_scale(magnitude<T>(top2<T>(m0, n0)), s, &f0);
+              const uint8_t s1 = block_scale(magnitude<T>(top2<T>(m1, n1)), s, &f1);
               const uint32_t o0 = e2m1x8_of<T>(w0, f0), o1 = e2m1x8_of<T>(w1, f1);
               if (live) {
                 codes[u0] = o0;
@@ -474,10 +479,10 @@ unsigned row_ctas(long long warps, int warps_per_token, int per_sm) {
   return (unsigned)(n > least ? n : least);
 }
 
-template <typename T, int FMT, int D>
+template <typename T, int FMT, int D, bool ROT>
 cudaError_t launch_append(const RopeArgs& a, int num_tokens, cudaStream_t stream) {
   constexpr int smem = kRowWarps * kRowStages * (kStageBytes + 8), PR = kTaskBytes / (2 * D);
-  auto* kern = rope_append_kernel<T, FMT, D>;
+  auto* kern = rope_append_kernel<T, FMT, D, ROT>;
   static std::atomic<uint64_t> configured{0};
   const cudaError_t e = allow_smem(kern, smem, &configured);
   if (e != cudaSuccess) return e;
@@ -516,7 +521,11 @@ cudaError_t dispatch(int dtype, int head_dim, int format, F f) {
 cudaError_t launch_rope_append(const RopeArgs& a, int dtype, int head_dim, int format, int num_tokens,
                                cudaStream_t stream, int* launches) {
   const cudaError_t e = dispatch(dtype, head_dim, format, [&](auto t, auto fmt, auto d) {
-    return launch_append<decltype(t), decltype(fmt)::value, decltype(d)::value>(a, num_tokens, stream);
+    using T = decltype(t);
+    constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
+    if constexpr (F == kFmtFp4)
+      if (a.rotary_dim == 0) return launch_append<T, F, D, false>(a, num_tokens, stream);
+    return launch_append<T, F, D, true>(a, num_tokens, stream);
   });
   if (e == cudaSuccess) ++*launches;
   return e;

@@ -169,9 +169,10 @@ def _check(fn: str, status: int) -> None:
 def _ptr(x) -> int | None:
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return x  # an address
 
 
 _current_stream = None
