@@ -1,24 +1,38 @@
 // pa_decode_fp4.cu -- single-token decode attention over an E2M1 cache.
 //
-// Work split.  An item is a (sequence, kv head) pair; its context is cut into chunks of
-// 64 tokens.  The chunks of all items, in order, are split evenly into one span
-// per worker: long and short contexts balance, and only an item cut by a
-// span's border needs merging.  A worker is a warp; or, where there are fewer
+// Work split.  An item is a (sequence, kv head) pair; its context is cut into
+// chunks of 64 tokens.  The chunks of all items, in order, are split evenly into
+// one span per worker: long and short contexts balance, and only an item cut by
+// a span's border needs merging.  A worker is a warp; or, where there are fewer
 // items than CTAs, a team: the four warps of a CTA, which claim a span's chunks
-// one by one and merge through shared memory at an item's end.  (Warps of one SM
-// differ by 10 percent in what they get through; a team evens that out, and
-// cuts an item into a quarter of the parts.)  A worker finds its span by a scan over the
-// context lengths.  A warp runs its own ring of bulk copies, across items: a
+// one by one and merge through shared memory at an item's end.  (Warps of one
+// SM differ by some 7 percent in what they get through; a team evens that out,
+// and cuts an item into a quarter of the parts: one sequence of 1000 tokens,
+// 8 kv heads, takes 8.4 us against 10.8.)  A worker finds its span by a scan over the
+// context lengths.
+//
+// Copies.  A warp runs its own ring of two stages of bulk copies, across items: a
 // (block, head) run is contiguous, so a chunk of K is one copy per block (two
 // where a block holds more than the copy: codes, then block scales), one lane
 // each, and table entries are read one chunk ahead.
 //
 // A cut item's parts are merged as they arrive: the parts form a tree of 8
-// children a node; a worker publishes its partial result, counts itself in at the
-// node, and the last one in combines the children, in order, and goes on to the
-// node above with the result, so the outcome does not depend on who came
-// last.  Nobody waits.  (A kernel of its own for this cost 8 to 12 us at 64 to 128
-// sequences: its loads start only when the last span has ended.)
+// children a node; a worker publishes its partial result, counts itself in at
+// the node, and the last one in combines the children, in order, and goes on to
+// the node above with the result, so the outcome does not depend on who came
+// last.  Nobody waits.  (A kernel of its own for this cost 8 to 12 us at 64 to
+// 128 sequences: its loads start only when the last span has ended.)
+//
+// What bounds it, on a B200 (128 sequences of 1024 to 4096 tokens, 32/8 heads of
+// 128, bf16; 377 MB, 57.6 us at 6551 GB/s): 87 us, 4.3 TB/s.  Without the
+// arithmetic the same copies take 70 us: 2 us of launch and scan, 61 of streaming at
+// 6.2 TB/s, the rest the first copies' latency and the last warp's lead.  The
+// arithmetic (285 instructions a warp for 16 tokens, 132 of them on the pipe of
+// conversions and logic) then fits between the copies but for some 17 us, 5 of them
+// the merges of cut items.  Measured and not kept: 16 warps per SM with chunks of
+// 32 tokens (the work per chunk doubles: 98 us), producer warps that issue the
+// copies for twelve others (111 us), one lane issuing all of a warp's copies (93 us),
+// small spans claimed at the end (103 us).
 //
 // Both products run as m16n8k16 matrix instructions in f16 with fp32 sums, the
 // cache always on the 16-row side and the group's query heads on the 8-column side:
@@ -32,13 +46,20 @@
 //   K: thread (g, t) = (lane / 4, lane % 4) holds dims [t D/4, (t + 1) D/4) of
 //      the tile's tokens perm(g) and perm(g) + 8;
 //   V: thread (g, t) holds dims [g D/8, (g + 1) D/8) of tokens t, t + 4, t + 8, t + 12;
-//      nibbles of two tokens are paired into bytes (one shift and one 3-input
-//      logic op per four) before widening, since a register pairs tokens.
+//      A register holds two neighbours of the contraction.  Up to groups of 8
+//      these are the two dims of a byte: the contraction runs over (token,
+//      parity of the dim), against a column that holds p for one parity and 0 for
+//      the other, so the output's columns are (head, parity): 8 of them for 4 heads,
+//      16 for 8.  For 16 heads that would take 32 columns and twice the matrix
+//      instructions, which bound that case; there nibbles of two tokens are paired
+//      into bytes (one shift and one 3-input logic op per four) before widening.
 // The 8 x 8 transposes from S^T's layout to P^T's are one movmatrix each.
 //
-// Softmax per warp in the log2 domain.  The reference m of a head moves only when a
-// logit exceeds it by more than 2^8: p <= 256 stays within f16, and the warp-wide
-// maximum and rescaling are rare.  Any m gives the same quotient.
+// Softmax per warp in the log2 domain.  The reference m of a head lies 7 below a
+// maximum and moves only when a logit exceeds it by more than 15: p <= 2^15 stays
+// within f16, the warp-wide maximum and rescaling are rare, and with a sum of 2^7 at
+// least f16's smallest step, 2^-24, is 2^-31 of it: what many tiny p lose to
+// rounding stays below 2^-12 up to a million tokens.  Any m gives the same quotient.
 //
 // Roundings: q is bf16 or f16; a bf16 row is scaled by a power of two to a
 // largest magnitude in [2^14, 2^15) and is then exact in f16 down to 2^-29 of it.
@@ -467,7 +488,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
         for (int n = 0; n < NS; ++n) {
           top[n][0] = xs[n][0] * fmaxf(fmaxf(x[0][n][0], x[0][n][2]), fmaxf(x[1][n][0], x[1][n][2]));
           top[n][1] = xs[n][1] * fmaxf(fmaxf(x[0][n][1], x[0][n][3]), fmaxf(x[1][n][1], x[1][n][3]));
-          grow |= top[n][0] > m[n][0] + 8.f || top[n][1] > m[n][1] + 8.f;
+          grow |= top[n][0] > m[n][0] + 15.f || top[n][1] > m[n][1] + 15.f;
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -477,7 +498,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
               float v = top[n][j];
 #pragma unroll
               for (int d = 4; d <= 16; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-              const float mn = fmaxf(m[n][j], v), al = ex2(m[n][j] - mn);
+              const float mn = fmaxf(m[n][j], v - 7.f), al = ex2(m[n][j] - mn);
               m[n][j] = mn;
               l[n][j] *= al;
 #pragma unroll
