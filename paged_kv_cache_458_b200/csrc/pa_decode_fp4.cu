@@ -5,7 +5,8 @@
 // one span per worker: long and short contexts balance, and only an item cut by
 // a span's border needs merging.  A worker is a warp; or, where there are fewer
 // items than CTAs, a team: the four warps of a CTA, which claim a span's chunks
-// one by one and merge through shared memory at an item's end.  (Warps of one
+// one by one and merge through shared memory at an item's end; whole items of few
+// chunks (kFp4Solo) go to one warp, without a merge.  (Warps of one
 // SM differ by some 7 percent in what they get through; a team evens that out,
 // and cuts an item into a quarter of the parts: one sequence of 1000 tokens,
 // 8 kv heads, takes 8.4 us against 10.8.)  A worker finds its span by a scan over the
@@ -82,6 +83,7 @@ constexpr int kFp4Chunk = 64;   // tokens a stage holds
 constexpr int kFp4Stages = 2;   // per warp
 constexpr int kFp4Ctas = 3;     // per SM, by registers and (D = 128) shared memory
 constexpr int kFp4Radix = 8;    // children of a merge node
+constexpr int kFp4Solo = 4;     // chunks of an item that a team leaves to one warp, at most (8 measured slower)
 
 template <int D>
 struct Fp4Smem {
@@ -229,6 +231,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   // The copies' cursor: the next chunk to fetch, its item, chunk number there and context;
   // this lane's group in it: its table entry and its offset in the block.
   int f_at = span_begin, f_seq = seq, f_head, f_chunk, f_ctx = context(seq), f_off;
+  [[maybe_unused]] int own_left = 0;  // team: further chunks of a short item of this warp's
   const int32_t* f_entry;          // of the group in the block table
   const int step_idx = CT / bs, step_off = CT - step_idx * bs;
   auto place = [&]() {
@@ -267,13 +270,28 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   auto fetch = [&]() {
     Group e{span_end, 0, -1, 0};
     if constexpr (TEAM) {
-      int c = 0;
-      if (lane == 0) c = atomicAdd(claims, 1);
-      c = __shfl_sync(0xffffffffu, c, 0);
-      if (c >= span_end) return e;
-      f_chunk += c - f_at;
-      f_at = c;
-      if (!settle()) place();
+      int c = f_at + 1;  // of a short item of this warp's
+      if (own_left > 0) --own_left;
+      else own_left = -1;
+      for (;;) {
+        if (own_left < 0) {
+          if (lane == 0) c = atomicAdd(claims, 1);
+          c = __shfl_sync(0xffffffffu, c, 0);
+          if (c >= span_end) {
+            own_left = 0;
+            return e;
+          }
+        }
+        f_chunk += c - f_at;
+        f_at = c;
+        if (!settle()) place();
+        if (own_left >= 0) break;
+        const int n = (f_ctx + CT - 1) / CT, start = c - f_chunk;
+        const bool solo = n <= kFp4Solo && start >= span_begin && start + n <= span_end;
+        if (solo && f_chunk > 0) continue;  // its first chunk's claimer has the whole item
+        own_left = solo ? n - 1 : 0;
+        break;
+      }
     }
     if (TEAM || f_at < span_end) {
       e.chunk = f_at;
@@ -336,528 +354,554 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   Group next = fetch();
   for (;;) {
     const int item_chunks = (ctx + CT - 1) / CT, len = min(item_chunks - first, span_end - at);
-    // what may be copied by now: a team's stages are free for its merge at the item's end
-    const int copy_end = TEAM ? at + len : span_end;
-    while (issued - k < NST && next.chunk < copy_end) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      issue(next);
-      next = fetch();
-    }
-    const size_t head0 = (size_t)seq * a.num_q_heads + kvh * G;
-
-    // queries as column fragments: thread (g, t) holds dims [t D/4, (t + 1) D/4) of heads g, g + 8
-    // The logit scale is kept positive: its sign goes into the queries, and a zero scale zeroes them.
-    const float cscale = a.scale_log2 * __ldg(a.k_scale + kvh);
-    uint32_t bq[NS][KW * 4];
-    float xs[NS][2];  // logit scale of this thread's columns 2t, 2t + 1
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      const int h = kFolded ? g & 3 : n * 8 + g;  // folded: columns 4 .. 7 repeat the heads
-      uint32_t w[KW * 4];
-#pragma unroll
-      for (int i = 0; i < KW; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (h < G) v = *reinterpret_cast<const uint4*>(a.q + (head0 + h) * D + t * (D / 4) + i * 8);
-        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-      }
-      float down = 1.f;
-      if constexpr (!kLo) {
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < KW * 4; ++i) {
-          const float2 f = Elem<T>::to_f2(w[i]);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max((int)(__float_as_uint(top) >> 23), 15);  // 2^(e - 127) <= top
-        const float up = __uint_as_float((uint32_t)(268 - e) << 23);  // 2^(141 - e)
-        down = __uint_as_float((uint32_t)(e - 14) << 23);
-#pragma unroll
-        for (int i = 0; i < KW * 4; ++i) {
-          const float2 f = Elem<T>::to_f2(w[i]);
-          w[i] = f16x2_of(f.x * up, f.y * up);
-        }
-      }
-      const float c = cscale * down;
-#pragma unroll
-      for (int i = 0; i < KW * 4; ++i) bq[n][i] = c == 0.f ? 0u : c < 0.f ? w[i] ^ 0x80008000u : w[i];
-      const float pos = c == 0.f ? 1.f : fabsf(c);
-      xs[n][0] = __shfl_sync(0xffffffffu, pos, 8 * t);
-      xs[n][1] = __shfl_sync(0xffffffffu, pos, 8 * t + 4);
-    }
-
-    float o[MT][NV][4], m[NS][2], l[NS][2];
-    constexpr auto tile_of = [](int v) { return GT == 16 ? v : 0; };  // the logits' tile of an output tile
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][v][j] = 0.f;
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      m[n][0] = m[n][1] = -1e30f;
-      l[n][0] = l[n][1] = 0.f;
-    }
-
-    for (; k < issued; ++k) {
-      int chunk = ids[0];
-#pragma unroll
-      for (int i = 1; i < NST; ++i)
-        if (k % NST == i) chunk = ids[i];
-      if (chunk >= at + len) break;
-      if (failed) continue;
-      if (!mbar_wait(bar0 + (k % NST) * 8, (k / NST) & 1, a.err)) {
-        // let the copies in flight land, and start no more
-        for (int i = k + 1; i < issued; ++i) mbar_wait(bar0 + (i % NST) * 8, (i / NST) & 1, a.err);
-        next.chunk = span_end;
-        failed = true;
-        continue;
-      }
-      unsigned char* stage = stages + (k % NST) * L::kStageBytes;
-      const int n_valid = ctx - (first + chunk - at) * CT;  // of this chunk's tokens
-      if (n_valid < CT) {
-        // what lies behind the last token may be anything: codes are finite, V's scales need not be
-        for (int tok = n_valid + lane; tok < CT; tok += 32) {
-          unsigned char* sc = stage + L::kPoolBytes + tok / R * R * L::kTokenBytes + kScaleBase + tok % R * (D / 16);
-          if constexpr (D == 128) *reinterpret_cast<uint2*>(sc) = make_uint2(0, 0);
-          else *reinterpret_cast<uint32_t*>(sc) = 0;
-        }
-        __syncwarp();
-      }
-#pragma unroll 1
-      for (int half = 0; half < min(n_valid, CT); half += 32) {
-        const unsigned char* st = stage + half * L::kTokenBytes;
-
-        // ---- logits
-        float x[TILES][NS][4];
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-          uint32_t ca[KW], cb[KW], sa, sb;
-          const unsigned char* ka = st + k_code + i * kCodeTile;
-          const unsigned char* ks = st + k_sc + i * kScaleTile;
-          if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(ka), w = *reinterpret_cast<const uint4*>(ka + kCodeHalf);
-            ca[0] = u.x; ca[1] = u.y; ca[2] = u.z; ca[3] = u.w;
-            cb[0] = w.x; cb[1] = w.y; cb[2] = w.z; cb[3] = w.w;
-            sa = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(ks));
-            sb = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(ks + kScaleHalf));
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(ka), w = *reinterpret_cast<const uint2*>(ka + kCodeHalf);
-            ca[0] = u.x; ca[1] = u.y;
-            cb[0] = w.x; cb[1] = w.y;
-            sa = e4m3x2_to_h2(ks[0]);
-            sb = e4m3x2_to_h2(ks[kScaleHalf]);
-          }
-#pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            const uint32_t pick = w < 2 ? 0x1010 : 0x3232;  // scale of this word's 16 dims, twice
-            const uint32_t da = __byte_perm(sa, 0, pick), db = __byte_perm(sb, 0, pick);
-            uint32_t fa[4], fb[4];
-            e2m1x8_to_h2(ca[w], fa);
-            e2m1x8_to_h2(cb[w], fb);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              fa[j] = hmul2(fa[j], da);
-              fb[j] = hmul2(fb[j], db);
-            }
-#pragma unroll
-            for (int n = 0; n < NS; ++n) {
-              if (w == 0) mma_f16_first(x[i][n], fa[0], fb[0], fa[1], fb[1], bq[n][0], bq[n][1]);
-              else mma_f16(x[i][n], fa[0], fb[0], fa[1], fb[1], bq[n][4 * w], bq[n][4 * w + 1]);
-              mma_f16(x[i][n], fa[2], fb[2], fa[3], fb[3], bq[n][4 * w + 2], bq[n][4 * w + 3]);
-            }
-          }
-        }
-
-        // ---- softmax
-        bool grow = false;
-        float top[NS][2];
-        if (half + 32 > n_valid) {
-#pragma unroll
-          for (int n = 0; n < NS; ++n)
-#pragma unroll
-            for (int i = 0; i < TILES; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (half + i * 16 + k_row + (j >> 1) * 8 >= n_valid) x[i][n][j] = -INFINITY;
-          __syncwarp();
-        }
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
-          top[n][0] = xs[n][0] * fmaxf(fmaxf(x[0][n][0], x[0][n][2]), fmaxf(x[1][n][0], x[1][n][2]));
-          top[n][1] = xs[n][1] * fmaxf(fmaxf(x[0][n][1], x[0][n][3]), fmaxf(x[1][n][1], x[1][n][3]));
-          grow |= top[n][0] > m[n][0] + 15.f || top[n][1] > m[n][1] + 15.f;
-        }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int n = 0; n < NS; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float v = top[n][j];
-#pragma unroll
-              for (int d = 4; d <= 16; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-              const float mn = fmaxf(m[n][j], v - 7.f), al = ex2(m[n][j] - mn);
-              m[n][j] = mn;
-              l[n][j] *= al;
-#pragma unroll
-              for (int w = 0; w < NV; ++w)
-                if (tile_of(w) == n) {
-#pragma unroll
-                  for (int i = 0; i < MT; ++i) {
-                    o[i][w][j] *= al;
-                    o[i][w][j + 2] *= al;
-                  }
-                }
-            }
-        }
-
-        // ---- probabilities as column fragments, and O^T += V^T P^T
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-          uint32_t hi[NS][2], lo[NS][2];
-#pragma unroll
-          for (int n = 0; n < NS; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float p0 = ex2(fmaf(x[i][n][2 * j], xs[n][0], -m[n][0])), p1 = ex2(fmaf(x[i][n][2 * j + 1], xs[n][1], -m[n][1]));
-              l[n][0] += p0;
-              l[n][1] += p1;
-              const uint32_t h = f16x2_of(p0, p1);
-              hi[n][j] = transpose_8x8(h);
-              if constexpr (kLo) {
-                const float2 f = h2_to_f2(h);
-                lo[n][j] = transpose_8x8(f16x2_of(p0 - f.x, p1 - f.y));
-              }
-            }
-          const unsigned char* va = st + v_code + i * kCodeTile;
-          const unsigned char* vs = st + v_sc + i * kScaleTile;
-          uint32_t c[4][VW], sc[2];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {  // tokens t, t + 4, t + 8, t + 12 of the tile
-            const unsigned char* from = va + (r & 1) * 4 * (D / 2) + (r >> 1) * kCodeHalf;
-            if constexpr (D == 128) {
-              const uint2 u = *reinterpret_cast<const uint2*>(from);
-              c[r][0] = u.x; c[r][1] = u.y;
-            } else {
-              c[r][0] = *reinterpret_cast<const uint32_t*>(from);
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            sc[r] = e4m3x2_to_h2((uint16_t)(vs[r * kScaleHalf] | (vs[4 * (D / 16) + r * kScaleHalf] << 8)));
-          if constexpr (kPairs) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {  // 8 tokens a product: t and t + 4, then t + 8 and t + 12
-              const uint32_t s0 = __byte_perm(sc[r], 0, 0x1010), s1 = __byte_perm(sc[r], 0, 0x3232);
-              uint32_t b0[NV], b1[NV], d0[NV], d1[NV];
-#pragma unroll
-              for (int v = 0; v < NV; ++v) {
-                const uint32_t at_lo = kFolded ? pair_lo : v ? 0x1044 : 0x4410, at_hi = kFolded ? pair_hi : v ? 0x3244 : 0x4432;
-                b0[v] = __byte_perm(hi[0][r], 0, at_lo);
-                b1[v] = __byte_perm(hi[0][r], 0, at_hi);
-                if constexpr (kLo) {
-                  d0[v] = __byte_perm(lo[0][r], 0, at_lo);
-                  d1[v] = __byte_perm(lo[0][r], 0, at_hi);
-                }
-              }
-#pragma unroll
-              for (int w = 0; w < VW; ++w) {
-                uint32_t f0[4], f1[4];
-                e2m1x8_to_h2(c[2 * r][w], f0);
-                e2m1x8_to_h2(c[2 * r + 1][w], f1);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  f0[j] = hmul2(f0[j], s0);
-                  f1[j] = hmul2(f1[j], s1);
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                  for (int v = 0; v < NV; ++v) {
-                    mma_f16(o[2 * w + j][v], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], b0[v], b1[v]);
-                    if constexpr (kLo)
-                      mma_f16(o[2 * w + j][v], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], d0[v], d1[v]);
-                  }
-              }
-            }
-          } else {
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-              uint32_t ev[2][4], od[2][4];  // [token pair][j]: dims 2j and 2j + 1 of the word
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const uint32_t u0 = c[2 * r][w], u1 = c[2 * r + 1][w];
-                e2m1x8_to_h2((u0 & 0x0f0f0f0fu) | ((u1 << 4) & 0xf0f0f0f0u), ev[r]);
-                e2m1x8_to_h2(((u0 >> 4) & 0x0f0f0f0fu) | (u1 & 0xf0f0f0f0u), od[r]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  ev[r][j] = hmul2(ev[r][j], sc[r]);
-                  od[r][j] = hmul2(od[r][j], sc[r]);
-                }
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int n = 0; n < NS; ++n) {
-                  mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], hi[n][0], hi[n][1]);
-                  if constexpr (kLo)
-                    mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], lo[n][0], lo[n][1]);
-                }
-            }
-          }
-        }
-      }
-      __syncwarp();
-      // the stage is free again: refill it
-      if (next.chunk < copy_end) {
+    // a team leaves short whole items to the warp that has claimed them
+    const bool solo = TEAM && first == 0 && len == item_chunks && item_chunks <= kFp4Solo;
+    if (!solo || (next.chunk >= at && next.chunk < at + len)) {
+      // what may be copied by now: a team's stages are free for its merge at the item's end
+      const int copy_end = TEAM ? at + len : span_end;
+      while (issued - k < NST && next.chunk < copy_end) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         issue(next);
         next = fetch();
       }
-    }
+      const size_t head0 = (size_t)seq * a.num_q_heads + kvh * G;
 
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int d = 4; d <= 16; d <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], d);
-        if (failed) l[n][j] = __int_as_float(0x7fc00000);
-      }
-
-    // From here a warp holds the rows i = row0, row0 + rows_step, ... of the
-    // state o[i][v] (all of them, or a team's warp every fourth) and every m and l.
-    const int row0 = TEAM ? warp : 0;
-    constexpr int rows_step = TEAM ? NW : 1, ROWS = (MT + rows_step - 1) / rows_step;
-    float4 x[ROWS][NV];
-    auto has = [&](int i) { return !TEAM || row0 + i * rows_step < MT; };
-    auto at_row = [&](int i, int v) { return (v * MT + row0 + i * rows_step) * 32; };  // in a stored state
-    auto at_ml = [&](int n) { return (MT * NV + n) * 32; };
-    // adds w0, w1 (columns 2t, 2t + 1) times a stored state's rows
-    auto add = [](float4& to, const float4& v, float w0, float w1) {
-      to.x = fmaf(v.x, w0, to.x);
-      to.y = fmaf(v.y, w1, to.y);
-      to.z = fmaf(v.z, w0, to.z);
-      to.w = fmaf(v.w, w1, to.w);
-    };
-    if constexpr (TEAM) {
-      float4* state = reinterpret_cast<float4*>(stages) + lane;  // every warp's, in its own stages
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) state[(v * MT + i) * 32] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
-#pragma unroll
-      for (int n = 0; n < NS; ++n) state[at_ml(n)] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
-      __syncthreads();
-      const float4* of[NW];
-      float w0[NS][NW], w1[NS][NW];
-#pragma unroll
-      for (int w = 0; w < NW; ++w) of[w] = reinterpret_cast<const float4*>(smem + w * NST * L::kStageBytes) + lane;
+      // queries as column fragments: thread (g, t) holds dims [t D/4, (t + 1) D/4) of heads g, g + 8
+      // The logit scale is kept positive: its sign goes into the queries, and a zero scale zeroes them.
+      const float cscale = a.scale_log2 * __ldg(a.k_scale + kvh);
+      uint32_t bq[NS][KW * 4];
+      float xs[NS][2];  // logit scale of this thread's columns 2t, 2t + 1
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
-        float4 ml[NW];
-        m[n][0] = m[n][1] = -1e30f;
+        const int h = kFolded ? g & 3 : n * 8 + g;  // folded: columns 4 .. 7 repeat the heads
+        uint32_t w[KW * 4];
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          ml[w] = of[w][at_ml(n)];
-          m[n][0] = fmaxf(m[n][0], ml[w].x);
-          m[n][1] = fmaxf(m[n][1], ml[w].y);
+        for (int i = 0; i < KW; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (h < G) v = *reinterpret_cast<const uint4*>(a.q + (head0 + h) * D + t * (D / 4) + i * 8);
+          w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         }
-        l[n][0] = l[n][1] = 0.f;
+        float down = 1.f;
+        if constexpr (!kLo) {
+          float top = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          w0[n][w] = ex2(ml[w].x - m[n][0]);
-          w1[n][w] = ex2(ml[w].y - m[n][1]);
-          l[n][0] = fmaf(ml[w].z, w0[n][w], l[n][0]);
-          l[n][1] = fmaf(ml[w].w, w1[n][w], l[n][1]);
+          for (int i = 0; i < KW * 4; ++i) {
+            const float2 f = Elem<T>::to_f2(w[i]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = max((int)(__float_as_uint(top) >> 23), 15);  // 2^(e - 127) <= top
+          const float up = __uint_as_float((uint32_t)(268 - e) << 23);  // 2^(141 - e)
+          down = __uint_as_float((uint32_t)(e - 14) << 23);
+#pragma unroll
+          for (int i = 0; i < KW * 4; ++i) {
+            const float2 f = Elem<T>::to_f2(w[i]);
+            w[i] = f16x2_of(f.x * up, f.y * up);
+          }
         }
+        const float c = cscale * down;
+#pragma unroll
+        for (int i = 0; i < KW * 4; ++i) bq[n][i] = c == 0.f ? 0u : c < 0.f ? w[i] ^ 0x80008000u : w[i];
+        const float pos = c == 0.f ? 1.f : fabsf(c);
+        xs[n][0] = __shfl_sync(0xffffffffu, pos, 8 * t);
+        xs[n][1] = __shfl_sync(0xffffffffu, pos, 8 * t + 4);
       }
-#pragma unroll
-      for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          x[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!has(i)) continue;
-#pragma unroll
-          for (int w = 0; w < NW; ++w) add(x[i][v], of[w][at_row(i, v)], w0[tile_of(v)][w], w1[tile_of(v)][w]);
-        }
-    } else {
+
+      float o[MT][NV][4], m[NS][2], l[NS][2];
+      constexpr auto tile_of = [](int v) { return GT == 16 ? v : 0; };  // the logits' tile of an output tile
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) x[i][v] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
-    }
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][v][j] = 0.f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        m[n][0] = m[n][1] = -1e30f;
+        l[n][0] = l[n][1] = 0.f;
+      }
 
-    // ---- an item cut by span borders: merge what has arrived
-    bool whole_item = first == 0 && len == item_chunks;
-    if (!whole_item) {
-      // chunk e lies in the span of worker ceil((e + 1) workers / chunks) - 1
-      const int item_at = at - first;  // the item's first chunk
-      const int lead = (int)(((long long)(item_at + 1) * workers - 1) / chunks);
-      const int parts = (int)(((long long)(item_at + item_chunks) * workers - 1) / chunks) - lead + 1;
-      constexpr int kState = Fp4State<D, GT>::kBytes / 16;
-      // part p: slot 2 i + 1 of worker i = lead for the item's first part, 2 i for those that started before span i
-      auto slot = [&](int p) { return partials + (size_t)(2 * (lead + p) + (p == 0)) * kState + lane; };
-      int node = worker - lead, width = 1;  // this result stands for the parts [node, node + width)
-      for (;;) {
-        float4* mine = slot(node);
+      for (; k < issued; ++k) {
+        int chunk = ids[0];
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int i = 0; i < ROWS; ++i)
-            if (has(i)) __stcg(mine + at_row(i, v), x[i][v]);
-        if (row0 == 0) {
-#pragma unroll
-          for (int n = 0; n < NS; ++n) __stcg(mine + at_ml(n), make_float4(m[n][0], m[n][1], l[n][0], l[n][1]));
+        for (int i = 1; i < NST; ++i)
+          if (k % NST == i) chunk = ids[i];
+        if (chunk >= at + len) break;
+        if (failed) continue;
+        if (!mbar_wait(bar0 + (k % NST) * 8, (k / NST) & 1, a.err)) {
+          // let the copies in flight land, and start no more
+          for (int i = k + 1; i < issued; ++i) mbar_wait(bar0 + (i % NST) * 8, (i / NST) & 1, a.err);
+          next.chunk = span_end;
+          failed = true;
+          continue;
         }
-        // the node above: up to 8 children of this width, from part `up` on
-        int up, kids;
-        for (;;) {
-          up = node / (width * kFp4Radix) * (width * kFp4Radix);
-          kids = min(kFp4Radix, (parts - up + width - 1) / width);
-          if (kids > 1) break;
-          width *= kFp4Radix;  // an only child: nothing to merge at this level
-        }
-        __threadfence();
-        if constexpr (TEAM) __syncthreads();
-        else __syncwarp();
-        bool last = false;
-        if (TEAM ? threadIdx.x == 0 : lane == 0) {
-          // counted in the word of the second child's first span, under this call's tag
-          unsigned long long* word = arrivals + lead + up + width;
-          unsigned long long old = atomicAdd(word, 1ull);
-          if ((old & ~0xffull) != tag) {  // not opened yet: this call's first count replaces what was there
-            unsigned long long now = old + 1;
-            for (;;) {
-              const bool open = (now & ~0xffull) == tag;
-              old = atomicCAS(word, now, open ? now + 1 : tag | 1);
-              if (old == now) break;
-              now = old;
-            }
-            if ((old & ~0xffull) != tag) old = tag;
+        unsigned char* stage = stages + (k % NST) * L::kStageBytes;
+        const int n_valid = ctx - (first + chunk - at) * CT;  // of this chunk's tokens
+        if (n_valid < CT) {
+          // what lies behind the last token may be anything: codes are finite, V's scales need not be
+          for (int tok = n_valid + lane; tok < CT; tok += 32) {
+            unsigned char* sc = stage + L::kPoolBytes + tok / R * R * L::kTokenBytes + kScaleBase + tok % R * (D / 16);
+            if constexpr (D == 128) *reinterpret_cast<uint2*>(sc) = make_uint2(0, 0);
+            else *reinterpret_cast<uint32_t*>(sc) = 0;
           }
-          last = (int)(old & 0xff) + 1 == kids;
-          if (last) __stcg(word, 0ull);  // for a replay of the same call
-          if constexpr (TEAM) claims[1] = last;
+          __syncwarp();
         }
-        if constexpr (TEAM) {
-          __syncthreads();
-          last = *reinterpret_cast<volatile int*>(claims + 1) != 0;
-        } else {
-          last = __shfl_sync(0xffffffffu, (int)last, 0);
-        }
-        if (!last) break;
-        __threadfence();
-        // all children, in order, kBatch of them in flight
-        constexpr int kBatch = TEAM ? (GT == 16 ? 4 : 8) : GT == 4 ? 4 : GT == 8 ? 2 : 1;
-        for (int c0 = 0; c0 < kids; c0 += kBatch) {
-          float4 y[kBatch][ROWS][NV], ml[kBatch][NS];
+#pragma unroll 1
+        for (int half = 0; half < min(n_valid, CT); half += 32) {
+          const unsigned char* st = stage + half * L::kTokenBytes;
+
+          // ---- logits
+          float x[TILES][NS][4];
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const float4* from = slot(up + min(c0 + b, kids - 1) * width);
-#pragma unroll
-            for (int n = 0; n < NS; ++n) ml[b][n] = __ldcg(from + at_ml(n));
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-              for (int v = 0; v < NV; ++v)
-                if (has(i)) y[b][i][v] = __ldcg(from + at_row(i, v));
-          }
-          float a0[NS], a1[NS];  // weights of what has been added up so far
-#pragma unroll
-          for (int n = 0; n < NS; ++n) {
-            float m0 = c0 ? m[n][0] : -1e30f, m1 = c0 ? m[n][1] : -1e30f;
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-              m0 = fmaxf(m0, ml[b][n].x);
-              m1 = fmaxf(m1, ml[b][n].y);
-            }
-            a0[n] = ex2(m[n][0] - m0);
-            a1[n] = ex2(m[n][1] - m1);
-            m[n][0] = m0;
-            m[n][1] = m1;
-            l[n][0] = c0 ? l[n][0] * a0[n] : 0.f;
-            l[n][1] = c0 ? l[n][1] * a1[n] : 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              const float w0 = a0[tile_of(v)], w1 = a1[tile_of(v)];
-              x[i][v] = c0 ? make_float4(x[i][v].x * w0, x[i][v].y * w1, x[i][v].z * w0, x[i][v].w * w1)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < TILES; ++i) {
+            uint32_t ca[KW], cb[KW], sa, sb;
+            const unsigned char* ka = st + k_code + i * kCodeTile;
+            const unsigned char* ks = st + k_sc + i * kScaleTile;
+            if constexpr (D == 128) {
+              const uint4 u = *reinterpret_cast<const uint4*>(ka), w = *reinterpret_cast<const uint4*>(ka + kCodeHalf);
+              ca[0] = u.x; ca[1] = u.y; ca[2] = u.z; ca[3] = u.w;
+              cb[0] = w.x; cb[1] = w.y; cb[2] = w.z; cb[3] = w.w;
+              sa = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(ks));
+              sb = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(ks + kScaleHalf));
+            } else {
+              const uint2 u = *reinterpret_cast<const uint2*>(ka), w = *reinterpret_cast<const uint2*>(ka + kCodeHalf);
+              ca[0] = u.x; ca[1] = u.y;
+              cb[0] = w.x; cb[1] = w.y;
+              sa = e4m3x2_to_h2(ks[0]);
+              sb = e4m3x2_to_h2(ks[kScaleHalf]);
             }
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b)
-            if (c0 + b < kids) {
-              float w0[NS], w1[NS];
+            for (int w = 0; w < KW; ++w) {
+              const uint32_t pick = w < 2 ? 0x1010 : 0x3232;  // scale of this word's 16 dims, twice
+              const uint32_t da = __byte_perm(sa, 0, pick), db = __byte_perm(sb, 0, pick);
+              uint32_t fa[4], fb[4];
+              e2m1x8_to_h2(ca[w], fa);
+              e2m1x8_to_h2(cb[w], fb);
 #pragma unroll
-              for (int n = 0; n < NS; ++n) {
-                w0[n] = ex2(ml[b][n].x - m[n][0]);
-                w1[n] = ex2(ml[b][n].y - m[n][1]);
-                l[n][0] = fmaf(ml[b][n].z, w0[n], l[n][0]);
-                l[n][1] = fmaf(ml[b][n].w, w1[n], l[n][1]);
+              for (int j = 0; j < 4; ++j) {
+                fa[j] = hmul2(fa[j], da);
+                fb[j] = hmul2(fb[j], db);
               }
 #pragma unroll
-              for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-                  if (has(i)) add(x[i][v], y[b][i][v], w0[tile_of(v)], w1[tile_of(v)]);
+              for (int n = 0; n < NS; ++n) {
+                if (w == 0) mma_f16_first(x[i][n], fa[0], fb[0], fa[1], fb[1], bq[n][0], bq[n][1]);
+                else mma_f16(x[i][n], fa[0], fb[0], fa[1], fb[1], bq[n][4 * w], bq[n][4 * w + 1]);
+                mma_f16(x[i][n], fa[2], fb[2], fa[3], fb[3], bq[n][4 * w + 2], bq[n][4 * w + 3]);
+              }
             }
-        }
-        node = up;
-        width *= kFp4Radix;
-        if (width >= parts) {
-          whole_item = true;
-          break;
-        }
-        if constexpr (TEAM) __syncthreads();  // the children are read before the result takes the first one's slot
-      }
-    }
+          }
 
-    if (whole_item) {
-      const float v_scale = __ldg(a.v_scale + kvh);
-      auto pair = [](float v0, float v1) {
-        return (uint32_t)Elem<T>::from_f(v0) | ((uint32_t)Elem<T>::from_f(v1) << 16);
-      };
-      uint16_t* out = a.out + head0 * D + g * (D / 8);  // this thread's dims of head 0
+          // ---- softmax
+          bool grow = false;
+          float top[NS][2];
+          if (half + 32 > n_valid) {
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        if (!has(i)) continue;
-        const int row = row0 + i * rows_step;
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int i = 0; i < TILES; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (half + i * 16 + k_row + (j >> 1) * 8 >= n_valid) x[i][n][j] = -INFINITY;
+            __syncwarp();
+          }
+#pragma unroll
+          for (int n = 0; n < NS; ++n) {
+            top[n][0] = xs[n][0] * fmaxf(fmaxf(x[0][n][0], x[0][n][2]), fmaxf(x[1][n][0], x[1][n][2]));
+            top[n][1] = xs[n][1] * fmaxf(fmaxf(x[0][n][1], x[0][n][3]), fmaxf(x[1][n][1], x[1][n][3]));
+            grow |= top[n][0] > m[n][0] + 15.f || top[n][1] > m[n][1] + 15.f;
+          }
+          if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float v = top[n][j];
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                const float mn = fmaxf(m[n][j], v - 7.f), al = ex2(m[n][j] - mn);
+                m[n][j] = mn;
+                l[n][j] *= al;
+#pragma unroll
+                for (int w = 0; w < NV; ++w)
+                  if (tile_of(w) == n) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                      o[i][w][j] *= al;
+                      o[i][w][j + 2] *= al;
+                    }
+                  }
+              }
+          }
+
+          // ---- probabilities as column fragments, and O^T += V^T P^T
+#pragma unroll
+          for (int i = 0; i < TILES; ++i) {
+            uint32_t hi[NS][2], lo[NS][2];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float p0 = ex2(fmaf(x[i][n][2 * j], xs[n][0], -m[n][0])), p1 = ex2(fmaf(x[i][n][2 * j + 1], xs[n][1], -m[n][1]));
+                l[n][0] += p0;
+                l[n][1] += p1;
+                const uint32_t h = f16x2_of(p0, p1);
+                hi[n][j] = transpose_8x8(h);
+                if constexpr (kLo) {
+                  const float2 f = h2_to_f2(h);
+                  lo[n][j] = transpose_8x8(f16x2_of(p0 - f.x, p1 - f.y));
+                }
+              }
+            const unsigned char* va = st + v_code + i * kCodeTile;
+            const unsigned char* vs = st + v_sc + i * kScaleTile;
+            uint32_t c[4][VW], sc[2];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {  // tokens t, t + 4, t + 8, t + 12 of the tile
+              const unsigned char* from = va + (r & 1) * 4 * (D / 2) + (r >> 1) * kCodeHalf;
+              if constexpr (D == 128) {
+                const uint2 u = *reinterpret_cast<const uint2*>(from);
+                c[r][0] = u.x; c[r][1] = u.y;
+              } else {
+                c[r][0] = *reinterpret_cast<const uint32_t*>(from);
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              sc[r] = e4m3x2_to_h2((uint16_t)(vs[r * kScaleHalf] | (vs[4 * (D / 16) + r * kScaleHalf] << 8)));
+            if constexpr (kPairs) {
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {  // 8 tokens a product: t and t + 4, then t + 8 and t + 12
+                const uint32_t s0 = __byte_perm(sc[r], 0, 0x1010), s1 = __byte_perm(sc[r], 0, 0x3232);
+                uint32_t b0[NV], b1[NV], d0[NV], d1[NV];
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                  const uint32_t at_lo = kFolded ? pair_lo : v ? 0x1044 : 0x4410, at_hi = kFolded ? pair_hi : v ? 0x3244 : 0x4432;
+                  b0[v] = __byte_perm(hi[0][r], 0, at_lo);
+                  b1[v] = __byte_perm(hi[0][r], 0, at_hi);
+                  if constexpr (kLo) {
+                    d0[v] = __byte_perm(lo[0][r], 0, at_lo);
+                    d1[v] = __byte_perm(lo[0][r], 0, at_hi);
+                  }
+                }
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                  uint32_t f0[4], f1[4];
+                  e2m1x8_to_h2(c[2 * r][w], f0);
+                  e2m1x8_to_h2(c[2 * r + 1][w], f1);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    f0[j] = hmul2(f0[j], s0);
+                    f1[j] = hmul2(f1[j], s1);
+                  }
+#pragma unroll
+                  for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                      mma_f16(o[2 * w + j][v], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], b0[v], b1[v]);
+                      if constexpr (kLo)
+                        mma_f16(o[2 * w + j][v], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], d0[v], d1[v]);
+                    }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int w = 0; w < VW; ++w) {
+                uint32_t ev[2][4], od[2][4];  // [token pair][j]: dims 2j and 2j + 1 of the word
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const uint32_t u0 = c[2 * r][w], u1 = c[2 * r + 1][w];
+                  e2m1x8_to_h2((u0 & 0x0f0f0f0fu) | ((u1 << 4) & 0xf0f0f0f0u), ev[r]);
+                  e2m1x8_to_h2(((u0 >> 4) & 0x0f0f0f0fu) | (u1 & 0xf0f0f0f0u), od[r]);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    ev[r][j] = hmul2(ev[r][j], sc[r]);
+                    od[r][j] = hmul2(od[r][j], sc[r]);
+                  }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int n = 0; n < NS; ++n) {
+                    mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], hi[n][0], hi[n][1]);
+                    if constexpr (kLo)
+                      mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], lo[n][0], lo[n][1]);
+                  }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        // the stage is free again: refill it
+        if (next.chunk < copy_end) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          issue(next);
+          next = fetch();
+        }
+      }
+
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int d = 4; d <= 16; d <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], d);
+          if (failed) l[n][j] = __int_as_float(0x7fc00000);
+        }
+
+      // Writes the outputs of a row of the state: x[v] are its tiles, f the columns' factors.
+      auto emit = [&](int row, const float4 (&x)[NV], const float (&f)[NS][2]) {
+        auto pair = [](float v0, float v1) {
+          return (uint32_t)Elem<T>::from_f(v0) | ((uint32_t)Elem<T>::from_f(v1) << 16);
+        };
+        uint16_t* out = a.out + head0 * D + g * (D / 8);  // this thread's dims of head 0
 #pragma unroll
         for (int j = 0; j < 2; ++j) {  // columns 2t and 2t + 1
-          auto first_of = [&](int v) { return j ? x[i][v].y : x[i][v].x; };    // of the tile's row g
-          auto second_of = [&](int v) { return j ? x[i][v].w : x[i][v].z; };  // of row g + 8
+          auto first_of = [&](int v) { return j ? x[v].y : x[v].x; };   // of the tile's row g
+          auto second_of = [&](int v) { return j ? x[v].w : x[v].z; };  // of row g + 8
           if constexpr (kFolded) {
             // threads t < 2 hold the even dims of two pairs, t >= 2 the odd ones: each takes one pair
-            const float f = v_scale / l[0][j];
-            float v0 = first_of(0) * f, v1 = second_of(0) * f;
+            float v0 = first_of(0) * f[0][j], v1 = second_of(0) * f[0][j];
             const float got = __shfl_xor_sync(0xffffffffu, t < 2 ? v1 : v0, 2);
             if (t < 2) v1 = got;
             else v0 = got;
             const int h = 2 * (t & 1) + j;
             if (h < G) *reinterpret_cast<uint32_t*>(out + h * D + 4 * row + 2 * (t >> 1)) = pair(v0, v1);
           } else if constexpr (kPairs) {
-            const float f = v_scale / l[0][j];
             const int h = 2 * t + j;
             if (h < G)
               *reinterpret_cast<uint2*>(out + h * D + 4 * row) =
-                  make_uint2(pair(first_of(0) * f, first_of(1) * f), pair(second_of(0) * f, second_of(1) * f));
+                  make_uint2(pair(first_of(0) * f[0][j], first_of(1) * f[0][j]),
+                             pair(second_of(0) * f[0][j], second_of(1) * f[0][j]));
           } else {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-              const float f = v_scale / l[tile_of(v)][j];
+              const float fv = f[tile_of(v)][j];
               const int h = v * 8 + 2 * t + j;
-              if (h < G) *reinterpret_cast<uint32_t*>(out + h * D + 2 * row) = pair(first_of(v) * f, second_of(v) * f);
+              if (h < G) *reinterpret_cast<uint32_t*>(out + h * D + 2 * row) = pair(first_of(v) * fv, second_of(v) * fv);
             }
           }
         }
+      };
+      auto factors = [&](float (&f)[NS][2]) {
+        const float v_scale = __ldg(a.v_scale + kvh);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          f[n][0] = v_scale / l[n][0];
+          f[n][1] = v_scale / l[n][1];
+        }
+      };
+      if (solo) {
+        float f[NS][2];
+        factors(f);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          float4 y[NV];
+#pragma unroll
+          for (int v = 0; v < NV; ++v) y[v] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
+          emit(i, y, f);
+        }
+      } else {
+
+        // From here a warp holds the rows i = row0, row0 + rows_step, ... of the
+        // state o[i][v] (all of them, or a team's warp every fourth) and every m and l.
+        const int row0 = TEAM ? warp : 0;
+        constexpr int rows_step = TEAM ? NW : 1, ROWS = (MT + rows_step - 1) / rows_step;
+        float4 x[ROWS][NV];
+        auto has = [&](int i) { return !TEAM || row0 + i * rows_step < MT; };
+        auto at_row = [&](int i, int v) { return (v * MT + row0 + i * rows_step) * 32; };  // in a stored state
+        auto at_ml = [&](int n) { return (MT * NV + n) * 32; };
+        // adds w0, w1 (columns 2t, 2t + 1) times a stored state's rows
+        auto add = [](float4& to, const float4& v, float w0, float w1) {
+          to.x = fmaf(v.x, w0, to.x);
+          to.y = fmaf(v.y, w1, to.y);
+          to.z = fmaf(v.z, w0, to.z);
+          to.w = fmaf(v.w, w1, to.w);
+        };
+        if constexpr (TEAM) {
+          float4* state = reinterpret_cast<float4*>(stages) + lane;  // every warp's, in its own stages
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) state[(v * MT + i) * 32] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
+#pragma unroll
+          for (int n = 0; n < NS; ++n) state[at_ml(n)] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
+          __syncthreads();
+          const float4* of[NW];
+          float w0[NS][NW], w1[NS][NW];
+#pragma unroll
+          for (int w = 0; w < NW; ++w) of[w] = reinterpret_cast<const float4*>(smem + w * NST * L::kStageBytes) + lane;
+#pragma unroll
+          for (int n = 0; n < NS; ++n) {
+            float4 ml[NW];
+            m[n][0] = m[n][1] = -1e30f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+              ml[w] = of[w][at_ml(n)];
+              m[n][0] = fmaxf(m[n][0], ml[w].x);
+              m[n][1] = fmaxf(m[n][1], ml[w].y);
+            }
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+              w0[n][w] = ex2(ml[w].x - m[n][0]);
+              w1[n][w] = ex2(ml[w].y - m[n][1]);
+              l[n][0] = fmaf(ml[w].z, w0[n][w], l[n][0]);
+              l[n][1] = fmaf(ml[w].w, w1[n][w], l[n][1]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              x[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (!has(i)) continue;
+#pragma unroll
+              for (int w = 0; w < NW; ++w) add(x[i][v], of[w][at_row(i, v)], w0[tile_of(v)][w], w1[tile_of(v)][w]);
+            }
+        } else {
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) x[i][v] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
+        }
+
+        // ---- an item cut by span borders: merge what has arrived
+        bool whole_item = first == 0 && len == item_chunks;
+        if (!whole_item) {
+          // chunk e lies in the span of worker ceil((e + 1) workers / chunks) - 1
+          const int item_at = at - first;  // the item's first chunk
+          const int lead = (int)(((long long)(item_at + 1) * workers - 1) / chunks);
+          const int parts = (int)(((long long)(item_at + item_chunks) * workers - 1) / chunks) - lead + 1;
+          constexpr int kState = Fp4State<D, GT>::kBytes / 16;
+          // part p: slot 2 i + 1 of worker i = lead for the item's first part, 2 i for those that started before span i
+          auto slot = [&](int p) { return partials + (size_t)(2 * (lead + p) + (p == 0)) * kState + lane; };
+          int node = worker - lead, width = 1;  // this result stands for the parts [node, node + width)
+          for (;;) {
+            float4* mine = slot(node);
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+              for (int i = 0; i < ROWS; ++i)
+                if (has(i)) __stcg(mine + at_row(i, v), x[i][v]);
+            if (row0 == 0) {
+#pragma unroll
+              for (int n = 0; n < NS; ++n) __stcg(mine + at_ml(n), make_float4(m[n][0], m[n][1], l[n][0], l[n][1]));
+            }
+            // the node above: up to 8 children of this width, from part `up` on
+            int up, kids;
+            for (;;) {
+              up = node / (width * kFp4Radix) * (width * kFp4Radix);
+              kids = min(kFp4Radix, (parts - up + width - 1) / width);
+              if (kids > 1) break;
+              width *= kFp4Radix;  // an only child: nothing to merge at this level
+            }
+            __threadfence();
+            if constexpr (TEAM) __syncthreads();
+            else __syncwarp();
+            bool last = false;
+            if (TEAM ? threadIdx.x == 0 : lane == 0) {
+              // counted in the word of the second child's first span, under this call's tag
+              unsigned long long* word = arrivals + lead + up + width;
+              unsigned long long old = atomicAdd(word, 1ull);
+              if ((old & ~0xffull) != tag) {  // not opened yet: this call's first count replaces what was there
+                unsigned long long now = old + 1;
+                for (;;) {
+                  const bool open = (now & ~0xffull) == tag;
+                  old = atomicCAS(word, now, open ? now + 1 : tag | 1);
+                  if (old == now) break;
+                  now = old;
+                }
+                if ((old & ~0xffull) != tag) old = tag;
+              }
+              last = (int)(old & 0xff) + 1 == kids;
+              if (last) __stcg(word, 0ull);  // for a replay of the same call
+              if constexpr (TEAM) claims[1] = last;
+            }
+            if constexpr (TEAM) {
+              __syncthreads();
+              last = *reinterpret_cast<volatile int*>(claims + 1) != 0;
+            } else {
+              last = __shfl_sync(0xffffffffu, (int)last, 0);
+            }
+            if (!last) break;
+            __threadfence();
+            // all children, in order, kBatch of them in flight
+            constexpr int kBatch = TEAM ? (GT == 16 ? 4 : 8) : GT == 4 ? 4 : GT == 8 ? 2 : 1;
+            for (int c0 = 0; c0 < kids; c0 += kBatch) {
+              float4 y[kBatch][ROWS][NV], ml[kBatch][NS];
+#pragma unroll
+              for (int b = 0; b < kBatch; ++b) {
+                const float4* from = slot(up + min(c0 + b, kids - 1) * width);
+#pragma unroll
+                for (int n = 0; n < NS; ++n) ml[b][n] = __ldcg(from + at_ml(n));
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+                  for (int v = 0; v < NV; ++v)
+                    if (has(i)) y[b][i][v] = __ldcg(from + at_row(i, v));
+              }
+              float a0[NS], a1[NS];  // weights of what has been added up so far
+#pragma unroll
+              for (int n = 0; n < NS; ++n) {
+                float m0 = c0 ? m[n][0] : -1e30f, m1 = c0 ? m[n][1] : -1e30f;
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                  m0 = fmaxf(m0, ml[b][n].x);
+                  m1 = fmaxf(m1, ml[b][n].y);
+                }
+                a0[n] = ex2(m[n][0] - m0);
+                a1[n] = ex2(m[n][1] - m1);
+                m[n][0] = m0;
+                m[n][1] = m1;
+                l[n][0] = c0 ? l[n][0] * a0[n] : 0.f;
+                l[n][1] = c0 ? l[n][1] * a1[n] : 0.f;
+              }
+#pragma unroll
+              for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                  const float w0 = a0[tile_of(v)], w1 = a1[tile_of(v)];
+                  x[i][v] = c0 ? make_float4(x[i][v].x * w0, x[i][v].y * w1, x[i][v].z * w0, x[i][v].w * w1)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+              for (int b = 0; b < kBatch; ++b)
+                if (c0 + b < kids) {
+                  float w0[NS], w1[NS];
+#pragma unroll
+                  for (int n = 0; n < NS; ++n) {
+                    w0[n] = ex2(ml[b][n].x - m[n][0]);
+                    w1[n] = ex2(ml[b][n].y - m[n][1]);
+                    l[n][0] = fmaf(ml[b][n].z, w0[n], l[n][0]);
+                    l[n][1] = fmaf(ml[b][n].w, w1[n], l[n][1]);
+                  }
+#pragma unroll
+                  for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+                      if (has(i)) add(x[i][v], y[b][i][v], w0[tile_of(v)], w1[tile_of(v)]);
+                }
+            }
+            node = up;
+            width *= kFp4Radix;
+            if (width >= parts) {
+              whole_item = true;
+              break;
+            }
+            if constexpr (TEAM) __syncthreads();  // the children are read before the result takes the first one's slot
+          }
+        }
+
+        if (whole_item) {
+          float f[NS][2];
+          factors(f);
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i)
+            if (has(i)) emit(row0 + i * rows_step, x[i], f);
+        }
+        if constexpr (TEAM) __syncthreads();  // the stages are free for copies again
       }
     }
-    if constexpr (TEAM) __syncthreads();  // the stages are free for copies again
     at += len;
     if (at >= span_end) break;
     first = 0;
