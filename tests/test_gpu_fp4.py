@@ -192,6 +192,72 @@ def test_decode_long_context_and_many_sequences():
     assert_decode_close(_decode(c, gen.F16), ref.decode4(c, gen.F16), gen.F16, "many")
 
 
+@pytest.mark.parametrize("dtype,d,group,bs", [(gen.BF16, 128, 4, 16), (gen.F16, 64, 1, 8), (gen.F16, 128, 8, 64),
+                                              (gen.BF16, 64, 16, 24)])
+def test_decode_many_items_with_long_ones(dtype, d, group, bs):
+    """More items than CTAs: warps work alone; a long item among short ones is merged over several levels."""
+    rng = np.random.default_rng(20 + d + group)
+    ctx = rng.integers(0, 150, 160)
+    ctx[[3, 77]] = 9000, 2100
+    ctx[[0, 50, 159]] = 0
+    c = ref.quantised_case(rng, dtype=dtype, hq=3 * group, hkv=3, d=d, bs=bs, ctx=list(ctx))
+    exact = ref.decode4(c, dtype)
+    for pt in (0, 64, 640):
+        assert_decode_close(_decode(c, dtype, partition_tokens=pt), exact, dtype, f"partition {pt}")
+
+
+def test_decode_one_item_in_hundreds_of_parts():
+    rng = np.random.default_rng(30)
+    # a team per part: one item over all CTAs
+    c = ref.quantised_case(rng, dtype=gen.BF16, hq=2, hkv=1, d=64, bs=256, ctx=[100003])
+    exact = ref.decode4(c, gen.BF16)
+    for pt in (64, 0):
+        assert_decode_close(_decode(c, gen.BF16, partition_tokens=pt), exact, gen.BF16, f"partition {pt}")
+    # a warp per part: one long item among items of one token
+    c = ref.quantised_case(rng, dtype=gen.F16, hq=4, hkv=1, d=64, bs=16, ctx=[1] * 300 + [30001] + [1] * 200)
+    assert_decode_close(_decode(c, gen.F16), ref.decode4(c, gen.F16), gen.F16, "warps")
+
+
+@pytest.mark.parametrize("group,dtype", [(4, gen.BF16), (8, gen.F16), (16, gen.BF16)])
+def test_decode_few_ragged_items(group, dtype):
+    """Fewer items than CTAs, long and short: short whole items go to single warps, the rest to teams."""
+    rng = np.random.default_rng(40 + group)
+    c = ref.quantised_case(rng, dtype=dtype, hq=4 * group, hkv=4, d=128, bs=16,
+                           ctx=[64, 5, 0, 2000, 63, 65, 192, 256, 257, 320, 9, 8000, 1, 1, 1, 700])
+    exact = ref.decode4(c, dtype)
+    for pt in (0, 320, 2048):
+        assert_decode_close(_decode(c, dtype, partition_tokens=pt), exact, dtype, f"partition {pt}")
+
+
+def test_decode_uniform_tiny_probabilities():
+    """One key far above the others: what is left of 131072 equal, tiny probabilities must not round away."""
+    n, d, bs = 131072, 64, 256
+    rng = np.random.default_rng(50)
+    for dtype in (gen.BF16, gen.F16):
+        one = np.ones(1, F32)
+        c = ref.quantised_case(rng, dtype=dtype, hq=1, hkv=1, d=d, bs=bs, ctx=[n])
+        # K: rows of +1 (row 0) and of -1; V: 0 in row 0, 6 elsewhere; block scales 1
+        code_k, code_v = np.full((n, d), 10, np.uint8), np.full((n, d), 7, np.uint8)
+        code_k[0], code_v[0] = 2, 0
+        t = np.arange(n)
+        blk, off = c["block_tables"][0][t // bs], t % bs
+        for name, code in (("k", code_k), ("v", code_v)):
+            pool = ref.empty_pool4(c["num_blocks"], bs, 1, d, 0x38)  # E4M3 1.0
+            codes = np.zeros((c["num_blocks"], bs, d // 2), np.uint8)
+            codes[blk, off] = code[:, 0::2] | (code[:, 1::2] << 4)
+            pool[:, 0, :bs * d // 2] = codes.reshape(c["num_blocks"], -1)
+            c[name + "_pool"], c[name + "_scale"] = pool, one
+        c["q"] = gen.to_bits(np.ones((1, 1, d), F32), dtype)
+        # logits 64 s and -64 s: the others' probabilities are e^(-128 s), 2^-24 times 1.4 of the first one's
+        s = -np.log(1.4 * 2.0 ** -24) / 128
+        c["scale"] = float(F32(s))
+        exact = ref.decode4(c, dtype)
+        got = gen.bits_to_f32(_decode(c, dtype), dtype)
+        # the output's rounding, and 2^-10 for the probabilities' and the logits' (2^-16 absolute)
+        half = {gen.F16: 2.0 ** -11, gen.BF16: 2.0 ** -8}[dtype]
+        assert (np.abs(got - exact) <= np.abs(exact) * (half + 2.0 ** -10)).all(), (got.max(), exact.max())
+
+
 def test_decode_bound_above_the_contexts():
     """max_context_len is only a bound: a larger one gives the same attention."""
     rng = np.random.default_rng(3)
