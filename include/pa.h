@@ -157,7 +157,7 @@ typedef enum { PA_DECODE_AUTO = 0, PA_DECODE_CUDA_CORES = 1, PA_DECODE_TENSOR_CO
 
 /* The split-K partition pa_decode() uses for `shape` (partition_tokens, or
  * its default when 0), or minus the status pa_decode() would refuse the
- * shape with.  Host only. */
+ * shape with.  For an E2M1 cache see pa_decode_fp4().  Host only. */
 int pa_decode_partition_tokens(const pa_shape *shape);
 
 /* The kernel pa_decode() runs for `shape`: PA_DECODE_CUDA_CORES or
@@ -179,7 +179,8 @@ int pa_decode_resolved_variant(const pa_shape *shape);
  * / partition_tokens) partitions, two more with shared_prefix.  The
  * workspace needs no initialisation (the counter carries a per-call tag, so a
  * value left by an earlier call is recognised and replaced) and is dead after
- * the call's kernels finish.  Returns 0 for an invalid shape. */
+ * the call's kernels finish.  For an E2M1 cache (pa_decode_fp4) it holds two
+ * partial results and an arrival count per worker (33 MB at most).  Returns 0 for an invalid shape. */
 size_t pa_decode_workspace_bytes(const pa_shape *shape, int32_t max_context_len);
 
 /*
@@ -383,11 +384,15 @@ pa_status pa_cache_append_fp4(const void *k, const void *v, const int32_t *slot_
 /*
  * Decode attention over an E2M1 cache (shape->cache_format ==
  * PA_CACHE_FP4_E2M1, else PA_ERR_INVALID_ARG): pa_decode's result with K_j and
- * V_j the stored values.  Same workspace call as pa_decode.  Needs variant
- * PA_DECODE_AUTO and no shared_prefix (else PA_ERR_UNSUPPORTED).  With
- * partition_tokens 0 the partition follows from the batch and max_context_len
- * (at most 2048): the workspace must have been sized with this call's
- * max_context_len.
+ * V_j the stored values, in one launch.  Needs variant PA_DECODE_AUTO and no
+ * shared_prefix, blocks of less than 2^31 bytes, num_seqs and max_context_len up to
+ * 2^30 (else PA_ERR_UNSUPPORTED).  The batch's tokens are split evenly over the
+ * device whatever the contexts; partition_tokens is the least a warp takes (0:
+ * 64), and only bounds the split of small batches.  workspace: at least
+ * pa_decode_workspace_bytes(shape, max_context_len) bytes, with this call's
+ * shape and max_context_len; any contents; not shared with a decode that runs
+ * concurrently.  The same inputs give the same bits whatever the timing.
+ * Capture into a CUDA graph as pa_decode (no memset is added).
  */
 pa_status pa_decode_fp4(const void *q, const void *k_cache, const void *v_cache,
                         const float *k_scale, const float *v_scale,

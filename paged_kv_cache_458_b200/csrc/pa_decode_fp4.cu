@@ -85,6 +85,8 @@ constexpr int kFp4Ctas = 3;     // per SM, by registers and (D = 128) shared mem
 constexpr int kFp4Radix = 8;    // children of a merge node
 constexpr int kFp4Solo = 4;     // chunks of an item that a team leaves to one warp, at most (8 measured slower)
 
+constexpr float kFp4Lowest = -3.402823466e38f;  // reference before the first logit: fp32's lowest, so that any finite one raises it
+
 template <int D>
 struct Fp4Smem {
   static constexpr int kTokenBytes = D * 9 / 16;
@@ -132,6 +134,19 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// (x, y) *= (a, b) and += (a, b), each one packed instruction.
+__device__ __forceinline__ void mul_f32x2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmul.rn.f32x2 u, u, v;\n\t"
+      "mov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add_f32x2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\t"
+      "mov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -169,16 +184,34 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   const int S = a.num_seqs, Hkv = a.num_kv_heads, G = a.group;
   const int worker = TEAM ? blockIdx.x : blockIdx.x + gridDim.x * warp;
   auto context = [&](int s) { return max(0, min(__ldg(a.context_lens + s), a.max_context_len)); };
-  int sum = 0;
+  // lane i counts the chunks of the sequences [i run, (i + 1) run)
+  const int run = (S - 1) / 1024 * 32 + 32;
+  int run_sum = 0, run_at = 0, run_left = run;
   bool bad = false;
-#pragma unroll 4
-  for (int s = lane; s < S; s += 32) {
-    const int c = __ldg(a.context_lens + s);
-    bad |= c < 0 || c > a.max_context_len;
-    sum += (max(0, min(c, a.max_context_len)) + CT - 1) / CT;
+  for (int s0 = 0; s0 < S; s0 += 4 * 32) {
+    int n[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int s = s0 + j * 32 + lane, c = s < S ? __ldg(a.context_lens + s) : 0;
+      bad |= c < 0 || c > a.max_context_len;
+      n[j] = (max(0, min(c, a.max_context_len)) + CT - 1) / CT;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int sum = (int)__reduce_add_sync(0xffffffffu, (unsigned)n[j]);
+      if (lane == run_at) run_sum += sum;
+      if ((run_left -= 32) == 0) { ++run_at; run_left = run; }
+    }
   }
   if (bad && blockIdx.x == 0 && warp == 0) report(a.err, kErrContextLen);
-  const int chunks = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum) * Hkv;  // below 2^31
+  run_sum *= Hkv;
+  int run_end = run_sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, run_end, d);
+    if (lane >= d) run_end += v;
+  }
+  const int chunks = __shfl_sync(0xffffffffu, run_end, 31);  // below 2^31
   const int workers = min(num_workers, chunks);  // so that no span among them is empty
   // sequences without tokens: zero rows
   for (int s = blockIdx.x + gridDim.x * warp; s < S; s += gridDim.x * NW)
@@ -197,8 +230,9 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
     if (threadIdx.x == 0) claims[0] = span_begin;
     __syncthreads();
   }
-  // the sequence of chunk span_begin, and the number of its first chunk: 32 sequences at a time
-  int seq = 0, seq_base = 0;
+  // the sequence of chunk span_begin, and the number of its first chunk: its run, then 32 sequences at a time
+  const int in_run = __ffs(__ballot_sync(0xffffffffu, span_begin < run_end)) - 1;
+  int seq = in_run * run, seq_base = __shfl_sync(0xffffffffu, run_end - run_sum, in_run);
   for (;; seq += 32) {
     const int n = seq + lane < S ? (context(seq + lane) + CT - 1) / CT * Hkv : 0;
     int upto = n;
@@ -418,7 +452,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
           for (int j = 0; j < 4; ++j) o[i][v][j] = 0.f;
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
-        m[n][0] = m[n][1] = -1e30f;
+        m[n][0] = m[n][1] = kFp4Lowest;
         l[n][0] = l[n][1] = 0.f;
       }
 
@@ -505,11 +539,17 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
                   if (half + i * 16 + k_row + (j >> 1) * 8 >= n_valid) x[i][n][j] = -INFINITY;
             __syncwarp();
           }
+          // Scaled and rounded before the reference is taken off: fused, a logit of 2^28 or more would differ from its
+          // own rounded maximum by more than the exponentials' range.
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
-            top[n][0] = xs[n][0] * fmaxf(fmaxf(x[0][n][0], x[0][n][2]), fmaxf(x[1][n][0], x[1][n][2]));
-            top[n][1] = xs[n][1] * fmaxf(fmaxf(x[0][n][1], x[0][n][3]), fmaxf(x[1][n][1], x[1][n][3]));
-            grow |= top[n][0] > m[n][0] + 15.f || top[n][1] > m[n][1] + 15.f;
+#pragma unroll
+            for (int i = 0; i < TILES; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; j += 2) mul_f32x2(x[i][n][j], x[i][n][j + 1], xs[n][0], xs[n][1]);
+            top[n][0] = fmaxf(fmaxf(x[0][n][0], x[0][n][2]), fmaxf(x[1][n][0], x[1][n][2]));
+            top[n][1] = fmaxf(fmaxf(x[0][n][1], x[0][n][3]), fmaxf(x[1][n][1], x[1][n][3]));
+            grow |= top[n][0] - m[n][0] > 15.f || top[n][1] - m[n][1] > 15.f;
           }
           if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -542,7 +582,8 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
             for (int n = 0; n < NS; ++n)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const float p0 = ex2(fmaf(x[i][n][2 * j], xs[n][0], -m[n][0])), p1 = ex2(fmaf(x[i][n][2 * j + 1], xs[n][1], -m[n][1]));
+                add_f32x2(x[i][n][2 * j], x[i][n][2 * j + 1], -m[n][0], -m[n][1]);
+                const float p0 = ex2(x[i][n][2 * j]), p1 = ex2(x[i][n][2 * j + 1]);
                 l[n][0] += p0;
                 l[n][1] += p1;
                 const uint32_t h = f16x2_of(p0, p1);
@@ -733,7 +774,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
             float4 ml[NW];
-            m[n][0] = m[n][1] = -1e30f;
+            m[n][0] = m[n][1] = kFp4Lowest;
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
               ml[w] = of[w][at_ml(n)];
@@ -843,7 +884,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
               float a0[NS], a1[NS];  // weights of what has been added up so far
 #pragma unroll
               for (int n = 0; n < NS; ++n) {
-                float m0 = c0 ? m[n][0] : -1e30f, m1 = c0 ? m[n][1] : -1e30f;
+                float m0 = c0 ? m[n][0] : kFp4Lowest, m1 = c0 ? m[n][1] : kFp4Lowest;
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                   m0 = fmaxf(m0, ml[b][n].x);
@@ -966,7 +1007,7 @@ cudaError_t launch_fp4_dim(const DecodeArgs& a, int head_dim, const Fp4Launch& w
 bool fp4_decode_split(int num_seqs, int num_kv_heads, int max_context_len, int partition_tokens, Fp4Split* w) {
   *w = Fp4Split{1, 1, false};
   if (num_seqs == 0) return true;
-  if (max_context_len > 1 << 30) return false;
+  if (num_seqs > 1 << 30 || max_context_len > 1 << 30) return false;  // sums with a chunk or a scan's step stay in 31 bits
   const long long per_item = (max_context_len + kFp4Chunk - 1) / kFp4Chunk, items = (long long)num_seqs * num_kv_heads;
   if (items > 0x7fffffff || per_item * items > 0x7fffffffLL) return false;
   const int wave = 148 * kFp4Ctas;  // CTAs that a B200 holds at once

@@ -55,6 +55,12 @@ def test_decode_fp4_rejects_bad_arguments(lib, kw):
     assert _decode(lib, _shape(), **kw) == INVALID
 
 
+def test_decode_fp4_refuses_more_than_2_to_the_30_sequences_or_tokens(lib):
+    one = dict(num_q_heads=1, num_kv_heads=1, max_blocks_per_seq=(1 << 27) + 1)
+    assert _decode(lib, _shape(num_seqs=(1 << 30) + 1, **one), maxlen=16) == UNSUPPORTED
+    assert _decode(lib, _shape(num_seqs=1, **one), maxlen=(1 << 30) + 1) == UNSUPPORTED
+
+
 def test_decode_fp4_of_no_sequences_launches_nothing(lib):
     n = pa.pa_kernel_launches()
     assert _decode(lib, _shape(num_seqs=0), q=None) == OK

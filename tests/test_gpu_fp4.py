@@ -310,6 +310,31 @@ def test_decode_sharp_and_growing_logits():
             assert_decode_close(_decode(c, dtype, partition_tokens=pt), ref.decode4(c, dtype), dtype, f"pt {pt}")
 
 
+@pytest.mark.parametrize("dtype", [gen.F16, gen.BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("group,ctx", [(4, 300), (8, 70), (16, 2000)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_decode_logits_beyond_the_resolution_of_fp32(dtype, group, ctx, sign):
+    """Logits of 2^20 to 2^123, where one step of fp32 is more than any exponent that the kernel may form.
+
+    The keys have two values, one half of the other, and the queries are 1 or -1: every product and sum is exact, the
+    largest logits are equal and the others away by 2^19 at least, so the output is the mean of V over the former.
+    """
+    rng = np.random.default_rng(12)
+    bs, d, hkv = 16, 128, 1
+    c = ref.quantised_case(rng, dtype=dtype, hq=group * hkv, hkv=hkv, d=d, bs=bs, ctx=[ctx])
+    t = np.arange(ctx)
+    slots = c["block_tables"][0][t // bs].astype(np.int64) * bs + t % bs
+    x = np.where(t % 3 == 0, 6.0, 3.0).astype(F32)[:, None, None] * np.ones((1, hkv, d), F32)
+    c["k_scale"] = np.ones_like(c["k_scale"])
+    ref.store4(c["k_pool"], bs, d, slots, x, c["k_scale"])
+    c["q"] = gen.to_bits(np.full(c["q"].shape, sign, F32), dtype)
+    c["scale"] = 1.0
+    want = ref.decode4(c, dtype)
+    for e in range(12, 115):  # a key's dot product is 768 or 384
+        scale = float(F32(2.0 ** e * (1 + (e * 37 % 64) / 64 + 1 / 128 + 1 / 65536)))
+        assert_decode_close(_decode(c, dtype, scale=scale), want, dtype, f"2^{e}")
+
+
 @pytest.mark.parametrize("sign", [0.0, -1.0])
 def test_decode_zero_and_negative_scale(sign):
     rng = np.random.default_rng(7)
