@@ -3,22 +3,25 @@
 // Work split.  An item is a (sequence, kv head) pair; its context is cut into
 // chunks of 64 tokens.  The chunks of all items, in order, are split evenly into
 // one span per worker: long and short contexts balance, and only an item cut by
-// a span's border needs merging.  A worker is a warp; or, where there are fewer
-// items than CTAs, a team: the four warps of a CTA, which claim a span's chunks
-// one by one and merge through shared memory at an item's end; whole items of few
-// chunks (kFp4Solo) go to one warp, without a merge.  (Warps of one
-// SM differ by some 7 percent in what they get through; a team evens that out,
-// and cuts an item into a quarter of the parts: one sequence of 1000 tokens,
-// 8 kv heads, takes 8.4 us against 10.8.)  A worker finds its span by a scan over the
-// context lengths.
+// a span's border needs merging.  A worker finds its span by a scan over the
+// context lengths.  A worker is a warp; or, at groups of more than 8 heads where there
+// are fewer items than CTAs, a team: the four warps of a CTA, which claim a span's
+// chunks one by one and merge through shared memory at an item's end; whole items
+// of few chunks (kFp4Solo) go to one warp, without a merge.  A team cuts an item into a
+// quarter of the parts, and its warps share the merge of states that are twice or four
+// times as large there: 32 sequences of 8000 to 8192 tokens, 64/4 heads, take
+// 74 us against 103 by warps, one of 4000 21 against 25.  At smaller groups the
+// parts are cheap and a team's own merge is what costs: one sequence of 300 tokens,
+// 32/8 heads, 13.7 us by teams and 9.1 by warps, 18 of 300 to 16000 63 and
+// 48, 6 of 40000 to 131071 with 64/8 heads 125 and 128, one of 60000 30.5 and 32.4.
 //
 // Copies.  A warp runs its own ring of two stages of bulk copies, across items: a
 // (block, head) run is contiguous, so a chunk of K is one copy per block (two
 // where a block holds more than the copy: codes, then block scales), one lane
 // each, and table entries are read one chunk ahead.
 //
-// A cut item's parts are merged as they arrive: the parts form a tree of 8
-// children a node; a worker publishes its partial result, counts itself in at
+// A cut item's parts are merged as they arrive: the parts form a tree (see
+// kFp4Radix); a worker publishes its partial result, counts itself in at
 // the node, and the last one in combines the children, in order, and goes on to
 // the node above with the result, so the outcome does not depend on who came
 // last.  Nobody waits.  (A kernel of its own for this cost 8 to 12 us at 64 to
@@ -82,7 +85,10 @@ constexpr int kFp4Warps = 4;
 constexpr int kFp4Chunk = 64;   // tokens a stage holds
 constexpr int kFp4Stages = 2;   // per warp
 constexpr int kFp4Ctas = 3;     // per SM, by registers and (D = 128) shared memory
-constexpr int kFp4Radix = 8;    // children of a merge node
+// Children of a merge node, at most: 8; but with a state small enough for four children in flight (GT = 4), all parts of an
+// item of up to 24, so that one level does: a level costs some 2 us, a child 0.15 (16 parts of 64 tokens, 8 heads: 10.5 us
+// against 11.5 with nodes of 8; 64 parts: nodes of 8 15.5, of 16 16.2, of 32 18.2; GT = 8, 25 parts: 26.3, 28.0, 31.9).
+constexpr int kFp4Wide = 24, kFp4Radix = 8;
 constexpr int kFp4Solo = 4;     // chunks of an item that a team leaves to one warp, at most (8 measured slower)
 
 constexpr float kFp4Lowest = -3.402823466e38f;  // reference before the first logit: fp32's lowest, so that any finite one raises it
@@ -813,6 +819,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
           const int item_at = at - first;  // the item's first chunk
           const int lead = (int)(((long long)(item_at + 1) * workers - 1) / chunks);
           const int parts = (int)(((long long)(item_at + item_chunks) * workers - 1) / chunks) - lead + 1;
+          const int radix = GT == 4 && parts <= kFp4Wide ? kFp4Wide : kFp4Radix;
           constexpr int kState = Fp4State<D, GT>::kBytes / 16;
           // part p: slot 2 i + 1 of worker i = lead for the item's first part, 2 i for those that started before span i
           auto slot = [&](int p) { return partials + (size_t)(2 * (lead + p) + (p == 0)) * kState + lane; };
@@ -828,13 +835,13 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 #pragma unroll
               for (int n = 0; n < NS; ++n) __stcg(mine + at_ml(n), make_float4(m[n][0], m[n][1], l[n][0], l[n][1]));
             }
-            // the node above: up to 8 children of this width, from part `up` on
+            // the node above: up to `radix` children of this width, from part `up` on
             int up, kids;
             for (;;) {
-              up = node / (width * kFp4Radix) * (width * kFp4Radix);
-              kids = min(kFp4Radix, (parts - up + width - 1) / width);
+              up = node / (width * radix) * (width * radix);
+              kids = min(radix, (parts - up + width - 1) / width);
               if (kids > 1) break;
-              width *= kFp4Radix;  // an only child: nothing to merge at this level
+              width *= radix;  // an only child: nothing to merge at this level
             }
             __threadfence();
             if constexpr (TEAM) __syncthreads();
@@ -867,7 +874,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
             if (!last) break;
             __threadfence();
             // all children, in order, kBatch of them in flight
-            constexpr int kBatch = TEAM ? (GT == 16 ? 4 : 8) : GT == 4 ? 4 : GT == 8 ? 2 : 1;
+            constexpr int kBatch = TEAM ? 4 : GT == 4 ? 4 : GT == 8 ? 2 : 1;
             for (int c0 = 0; c0 < kids; c0 += kBatch) {
               float4 y[kBatch][ROWS][NV], ml[kBatch][NS];
 #pragma unroll
@@ -924,7 +931,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
                 }
             }
             node = up;
-            width *= kFp4Radix;
+            width *= radix;
             if (width >= parts) {
               whole_item = true;
               break;
@@ -979,7 +986,9 @@ cudaError_t launch_fp4(const DecodeArgs& a, const Fp4Launch& w) {
 
 template <typename T, int D, int GT, int R>
 cudaError_t launch_fp4_team(const DecodeArgs& a, const Fp4Launch& w) {
-  return w.split.team ? launch_fp4<T, D, GT, R, true>(a, w) : launch_fp4<T, D, GT, R, false>(a, w);
+  if constexpr (GT == 16)
+    if (w.split.team) return launch_fp4<T, D, GT, R, true>(a, w);
+  return launch_fp4<T, D, GT, R, false>(a, w);
 }
 
 template <typename T, int D, int GT>
@@ -1004,14 +1013,14 @@ cudaError_t launch_fp4_dim(const DecodeArgs& a, int head_dim, const Fp4Launch& w
 
 }  // namespace
 
-bool fp4_decode_split(int num_seqs, int num_kv_heads, int max_context_len, int partition_tokens, Fp4Split* w) {
+bool fp4_decode_split(int num_seqs, int num_kv_heads, int group, int max_context_len, int partition_tokens, Fp4Split* w) {
   *w = Fp4Split{1, 1, false};
   if (num_seqs == 0) return true;
   if (num_seqs > 1 << 30 || max_context_len > 1 << 30) return false;  // sums with a chunk or a scan's step stay in 31 bits
   const long long per_item = (max_context_len + kFp4Chunk - 1) / kFp4Chunk, items = (long long)num_seqs * num_kv_heads;
   if (items > 0x7fffffff || per_item * items > 0x7fffffffLL) return false;
   const int wave = 148 * kFp4Ctas;  // CTAs that a B200 holds at once
-  w->team = items < wave;
+  w->team = group > 8 && items < wave;  // see the top of this file
   // a warp takes a chunk at least, or the caller's partition
   const int least = (partition_tokens > 0 ? (partition_tokens + kFp4Chunk - 1) / kFp4Chunk : 1) * (w->team ? kFp4Warps : 1);
   const long long most = (per_item * items + least - 1) / least, all = w->team ? wave : wave * kFp4Warps;

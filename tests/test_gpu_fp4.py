@@ -208,7 +208,7 @@ def test_decode_many_items_with_long_ones(dtype, d, group, bs):
 
 def test_decode_one_item_in_hundreds_of_parts():
     rng = np.random.default_rng(30)
-    # a team per part: one item over all CTAs
+    # one item over all warps
     c = ref.quantised_case(rng, dtype=gen.BF16, hq=2, hkv=1, d=64, bs=256, ctx=[100003])
     exact = ref.decode4(c, gen.BF16)
     for pt in (64, 0):
@@ -220,7 +220,7 @@ def test_decode_one_item_in_hundreds_of_parts():
 
 @pytest.mark.parametrize("group,dtype", [(4, gen.BF16), (8, gen.F16), (16, gen.BF16)])
 def test_decode_few_ragged_items(group, dtype):
-    """Fewer items than CTAs, long and short: short whole items go to single warps, the rest to teams."""
+    """Few items, long and short: some cut into many parts, some whole within a warp's span."""
     rng = np.random.default_rng(40 + group)
     c = ref.quantised_case(rng, dtype=dtype, hq=4 * group, hkv=4, d=128, bs=16,
                            ctx=[64, 5, 0, 2000, 63, 65, 192, 256, 257, 320, 9, 8000, 1, 1, 1, 700])
