@@ -112,7 +112,7 @@ pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
     if (s->variant != PA_DECODE_AUTO || s->shared_prefix) return PA_ERR_UNSUPPORTED;
     pa::Fp4Split split;
     if (s->num_seqs > 0x7fffffff / s->num_q_heads || cache_block_bytes(s) >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
-    return pa::fp4_decode_split(s->num_seqs, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, max_context_len,
+    return pa::fp4_decode_split(s->num_seqs, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, s->head_dim, max_context_len,
                                 s->partition_tokens, &split)
                ? PA_OK : PA_ERR_UNSUPPORTED;
   }
@@ -201,7 +201,7 @@ struct Fp4Workspace {
 };
 Fp4Workspace fp4_workspace(const pa_shape* s, int32_t max_context_len) {
   Fp4Workspace w;
-  pa::fp4_decode_split(s->num_seqs, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, max_context_len, s->partition_tokens,
+  pa::fp4_decode_split(s->num_seqs, s->num_kv_heads, s->num_q_heads / s->num_kv_heads, s->head_dim, max_context_len, s->partition_tokens,
                        &w.split);
   w.arrivals = 2LL * w.split.workers * pa::fp4_state_bytes(s->head_dim, s->num_q_heads / s->num_kv_heads);
   w.bytes = w.arrivals + 8LL * w.split.workers;

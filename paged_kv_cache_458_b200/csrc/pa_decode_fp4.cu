@@ -9,8 +9,8 @@
 // chunks one by one and merge through shared memory at an item's end; whole items
 // of few chunks (kFp4Solo) go to one warp, without a merge.  A team cuts an item into a
 // quarter of the parts, and its warps share the merge of states that are twice or four
-// times as large there: 32 sequences of 8000 to 8192 tokens, 64/4 heads, take
-// 74 us against 103 by warps, one of 4000 21 against 25.  At smaller groups the
+// times as large there: 32 sequences of 8000 to 8192 tokens, 64/4 heads of 64, take
+// 42 us against 44.5 by warps, 8 of 50 to 8000 19 against 25.  At smaller groups the
 // parts are cheap and a team's own merge is what costs: one sequence of 300 tokens,
 // 32/8 heads, 13.7 us by teams and 9.1 by warps, 18 of 300 to 16000 63 and
 // 48, 6 of 40000 to 131071 with 64/8 heads 125 and 128, one of 60000 30.5 and 32.4.
@@ -84,7 +84,9 @@ namespace pa {
 constexpr int kFp4Warps = 4;
 constexpr int kFp4Chunk = 64;   // tokens a stage holds
 constexpr int kFp4Stages = 2;   // per warp
-constexpr int kFp4Ctas = 3;     // per SM, by registers and (D = 128) shared memory
+// CTAs per SM: 3, by registers and (D = 128) shared memory; 2 where the state of 16 heads of 128 takes 64 registers of a thread,
+// which at 168 spills in the products' loop (128 sequences of 1024 to 4096 tokens, 128/8 heads: 122 us against 197).
+constexpr int fp4_ctas(int head_dim, int group) { return head_dim == 128 && group > 8 ? 2 : 3; }
 // Children of a merge node, at most: 8; but with a state small enough for four children in flight (GT = 4), all parts of an
 // item of up to 24, so that one level does: a level costs some 2 us, a child 0.15 (16 parts of 64 tokens, 8 heads: 10.5 us
 // against 11.5 with nodes of 8; 64 parts: nodes of 8 15.5, of 16 16.2, of 32 18.2; GT = 8, 25 parts: 26.3, 28.0, 31.9).
@@ -160,7 +162,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // GT: the group's query heads, at most: 4, 8 or 16.  R: tokens of one copy.  TEAM: the CTA's warps share a span.
 template <typename T, int D, int GT, int R, bool TEAM>
-__global__ void __launch_bounds__(kFp4Warps * 32, kFp4Ctas)
+__global__ void __launch_bounds__(kFp4Warps * 32, fp4_ctas(D, GT))
 decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
                   const unsigned char* __restrict__ v_pool, const int num_workers, float4* partials,
                   unsigned long long* arrivals) {
@@ -1013,13 +1015,14 @@ cudaError_t launch_fp4_dim(const DecodeArgs& a, int head_dim, const Fp4Launch& w
 
 }  // namespace
 
-bool fp4_decode_split(int num_seqs, int num_kv_heads, int group, int max_context_len, int partition_tokens, Fp4Split* w) {
+bool fp4_decode_split(int num_seqs, int num_kv_heads, int group, int head_dim, int max_context_len, int partition_tokens,
+                      Fp4Split* w) {
   *w = Fp4Split{1, 1, false};
   if (num_seqs == 0) return true;
   if (num_seqs > 1 << 30 || max_context_len > 1 << 30) return false;  // sums with a chunk or a scan's step stay in 31 bits
   const long long per_item = (max_context_len + kFp4Chunk - 1) / kFp4Chunk, items = (long long)num_seqs * num_kv_heads;
   if (items > 0x7fffffff || per_item * items > 0x7fffffffLL) return false;
-  const int wave = 148 * kFp4Ctas;  // CTAs that a B200 holds at once
+  const int wave = 148 * fp4_ctas(head_dim, group);  // CTAs that a B200 holds at once
   w->team = group > 8 && items < wave;  // see the top of this file
   // a warp takes a chunk at least, or the caller's partition
   const int least = (partition_tokens > 0 ? (partition_tokens + kFp4Chunk - 1) / kFp4Chunk : 1) * (w->team ? kFp4Warps : 1);

@@ -179,7 +179,7 @@ struct Fp4Split {
   int ctas, workers;
   bool team;  // a worker is a CTA (else a warp)
 };
-bool fp4_decode_split(int num_seqs, int num_kv_heads, int group, int max_context_len, int partition_tokens,
+bool fp4_decode_split(int num_seqs, int num_kv_heads, int group, int head_dim, int max_context_len, int partition_tokens,
                       Fp4Split* split);
 int fp4_state_bytes(int head_dim, int group);
 cudaError_t launch_decode_fp4(const DecodeArgs& a, int dtype, int head_dim, const void* k_pool, const void* v_pool,
