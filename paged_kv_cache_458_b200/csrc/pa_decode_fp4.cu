@@ -4,16 +4,16 @@
 // chunks of 64 tokens.  The chunks of all items, in order, are split evenly into
 // one span per worker: long and short contexts balance, and only an item cut by
 // a span's border needs merging.  A worker finds its span by a scan over the
-// context lengths.  A worker is a warp; or, at groups of more than 8 heads where there
-// are fewer items than CTAs, a team: the four warps of a CTA, which claim a span's
+// context lengths.  A worker is a warp; or, at groups of more than 8 heads of 64
+// where there are fewer items than CTAs, a team: the four warps of a CTA, which claim a span's
 // chunks one by one and merge through shared memory at an item's end; whole items
 // of few chunks (kFp4Solo) go to one warp, without a merge.  A team cuts an item into a
-// quarter of the parts, and its warps share the merge of states that are twice or four
-// times as large there: 32 sequences of 8000 to 8192 tokens, 64/4 heads of 64, take
-// 42 us against 44.5 by warps, 8 of 50 to 8000 19 against 25.  At smaller groups the
-// parts are cheap and a team's own merge is what costs: one sequence of 300 tokens,
-// 32/8 heads, 13.7 us by teams and 9.1 by warps, 18 of 300 to 16000 63 and
-// 48, 6 of 40000 to 131071 with 64/8 heads 125 and 128, one of 60000 30.5 and 32.4.
+// quarter of the parts, and its warps share the merges: 32 sequences of 8000 to 8192 tokens,
+// 64/4 heads of 64, take 42 us against 44.5 by warps, 8 of 50 to 8000 19 against 25.  Elsewhere
+// a team's own merge and its uneven end cost more than they save: 4 sequences of 300 to 40000
+// tokens, 128/8 heads of 128, 63 us by teams and 52 by warps; one of 300 tokens,
+// 32/8 heads, 13.7 and 9.1; 18 of 300 to 16000 63 and 48; 6 of 40000 to
+// 131071 with 64/8 heads 125 and 128; one of 60000 30.5 and 32.4.
 //
 // Copies.  A warp runs its own ring of two stages of bulk copies, across items: a
 // (block, head) run is contiguous, so a chunk of K is one copy per block (two
@@ -988,7 +988,7 @@ cudaError_t launch_fp4(const DecodeArgs& a, const Fp4Launch& w) {
 
 template <typename T, int D, int GT, int R>
 cudaError_t launch_fp4_team(const DecodeArgs& a, const Fp4Launch& w) {
-  if constexpr (GT == 16)
+  if constexpr (GT == 16 && D == 64)
     if (w.split.team) return launch_fp4<T, D, GT, R, true>(a, w);
   return launch_fp4<T, D, GT, R, false>(a, w);
 }
@@ -1023,7 +1023,7 @@ bool fp4_decode_split(int num_seqs, int num_kv_heads, int group, int head_dim, i
   const long long per_item = (max_context_len + kFp4Chunk - 1) / kFp4Chunk, items = (long long)num_seqs * num_kv_heads;
   if (items > 0x7fffffff || per_item * items > 0x7fffffffLL) return false;
   const int wave = 148 * fp4_ctas(head_dim, group);  // CTAs that a B200 holds at once
-  w->team = group > 8 && items < wave;  // see the top of this file
+  w->team = head_dim == 64 && group > 8 && items < wave;  // see the top of this file
   // a warp takes a chunk at least, or the caller's partition
   const int least = (partition_tokens > 0 ? (partition_tokens + kFp4Chunk - 1) / kFp4Chunk : 1) * (w->team ? kFp4Warps : 1);
   const long long most = (per_item * items + least - 1) / least, all = w->team ? wave : wave * kFp4Warps;
