@@ -180,7 +180,7 @@ int pa_decode_resolved_variant(const pa_shape *shape);
  * workspace needs no initialisation (the counter carries a per-call tag, so a
  * value left by an earlier call is recognised and replaced) and is dead after
  * the call's kernels finish.  For an E2M1 cache (pa_decode_fp4) it holds two
- * partial results and an arrival count per worker (33 MB at most).  Returns 0 for an invalid shape. */
+ * partial results and an arrival count per worker (22 MB at most).  Returns 0 for an invalid shape. */
 size_t pa_decode_workspace_bytes(const pa_shape *shape, int32_t max_context_len);
 
 /*
