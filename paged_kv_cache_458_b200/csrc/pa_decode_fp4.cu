@@ -865,6 +865,8 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
               }
               last = (int)(old & 0xff) + 1 == kids;
               if (last) __stcg(word, 0ull);  // for a replay of the same call
+              // Orders the count before the reads below: here, then for the other threads by the barrier (a shuffle orders nothing).
+              __threadfence();
               if constexpr (TEAM) claims[1] = last;
             }
             if constexpr (TEAM) {
@@ -872,9 +874,9 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
               last = *reinterpret_cast<volatile int*>(claims + 1) != 0;
             } else {
               last = __shfl_sync(0xffffffffu, (int)last, 0);
+              __syncwarp();
             }
             if (!last) break;
-            __threadfence();
             // all children, in order, kBatch of them in flight
             constexpr int kBatch = TEAM ? 4 : GT == 4 ? 4 : GT == 8 ? 2 : 1;
             for (int c0 = 0; c0 < kids; c0 += kBatch) {
