@@ -155,6 +155,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t phase, unsigned
   return true;
 }
 
+// mbar_wait by a whole warp, with one verdict: lanes that judged the limit
+// apart would part ways before the warp's next shuffle or barrier, for good.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t phase, unsigned int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, phase, err));
+}
+
 // As mbar_wait, but also gives up (returning false) once *abort has been set
 // by another warp of the CTA; a timeout sets *abort itself.
 __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t phase, unsigned int* err,

@@ -471,7 +471,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
           if (k % NST == i) chunk = ids[i];
         if (chunk >= at + len) break;
         if (failed) continue;
-        if (!mbar_wait(bar0 + (k % NST) * 8, (k / NST) & 1, a.err)) {
+        if (!mbar_wait_warp(bar0 + (k % NST) * 8, (k / NST) & 1, a.err)) {
           // let the copies in flight land, and start no more
           for (int i = k + 1; i < issued; ++i) mbar_wait(bar0 + (i % NST) * 8, (i / NST) & 1, a.err);
           next.chunk = span_end;

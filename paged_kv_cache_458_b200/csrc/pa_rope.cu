@@ -248,7 +248,7 @@ rope_append_kernel(const RopeArgs a, const int num_tokens, const FastDiv by_bloc
   const long long kv_row = (long long)a.num_kv_heads * D * (FMT == kFmt16 ? 2 : 1);
   const long long run = fp4_head_bytes(a.block_size, D), block_bytes = run * a.num_kv_heads;
   for (int k = 0; k < n_mine; ++k) {
-    if (!mbar_wait(bar0 + stage_at * 8, phase, a.err)) {
+    if (!mbar_wait_warp(bar0 + stage_at * 8, phase, a.err)) {
       for (int i = k + 1; i < min(n_mine, k + kRowStages); ++i) {  // let the copies in flight land
         if (++stage_at == kRowStages) { stage_at = 0; phase ^= 1; }
         mbar_wait(bar0 + stage_at * 8, phase, a.err);
