@@ -5,9 +5,10 @@
 // one span per worker: long and short contexts balance, and only an item cut by
 // a span's border needs merging.  A worker finds its span by a scan over the
 // context lengths.  A worker is a warp; or, at groups of more than 8 heads of 64
-// where there are fewer items than CTAs, a team: the four warps of a CTA, which claim a span's
-// chunks one by one and merge through shared memory at an item's end; whole items
-// of few chunks (kFp4Solo) go to one warp, without a merge.  A team cuts an item into a
+// where there are fewer items than CTAs, a team: the four warps of a CTA, which take a span's
+// chunks in turn and merge through shared memory at an item's end; whole items
+// of few chunks (kFp4Solo) go to one warp, without a merge.  Which warp takes what is
+// fixed: chunks claimed by whoever came first gave other bits from call to call.  A team cuts an item into a
 // quarter of the parts, and its warps share the merges: 32 sequences of 8000 to 8192 tokens,
 // 64/4 heads of 64, take 42 us against 44.5 by warps, 8 of 50 to 8000 19 against 25.  Elsewhere
 // a team's own merge and its uneven end cost more than they save: 4 sequences of 300 to 40000
@@ -101,7 +102,7 @@ struct Fp4Smem {
   static constexpr int kPoolBytes = kFp4Chunk * kTokenBytes;  // K or V of one stage
   static constexpr int kStageBytes = 2 * kPoolBytes;
   static constexpr int kBars = kFp4Warps * kFp4Stages * kStageBytes;
-  static constexpr int kTeam = kBars + kFp4Warps * kFp4Stages * 8;  // next chunk to claim; merge verdict
+  static constexpr int kTeam = kBars + kFp4Warps * kFp4Stages * 8;  // a team's merge verdict
   static constexpr int kTotal = kTeam + 16;
 };
 
@@ -233,11 +234,10 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   // opens this span's arrival word: no count of another call is above the tag, and one of this call's stays
   const unsigned long long tag = a.epoch << 8;
   if (lane == 0) atomicMax(arrivals + worker, tag);
-  int* claims = reinterpret_cast<int*>(smem + L::kTeam);
-  if constexpr (TEAM) {
-    if (threadIdx.x == 0) claims[0] = span_begin;
-    __syncthreads();
-  }
+  // Team: a span's chunks go to its warps by number, all of a short whole item's to one warp, items in turn: which warp
+  // adds what up is fixed, and with it every bit of the sums.
+  auto one_warps = [&](int start, int n) { return TEAM && n <= kFp4Solo && start >= span_begin && start + n <= span_end; };
+  auto owner = [&](int s, int head) { return (s * Hkv + head) % NW; };
   // the sequence of chunk span_begin, and the number of its first chunk: its run, then 32 sequences at a time
   const int in_run = __ffs(__ballot_sync(0xffffffffu, span_begin < run_end)) - 1;
   int seq = in_run * run, seq_base = __shfl_sync(0xffffffffu, run_end - run_sum, in_run);
@@ -273,7 +273,6 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   // The copies' cursor: the next chunk to fetch, its item, chunk number there and context;
   // this lane's group in it: its table entry and its offset in the block.
   int f_at = span_begin, f_seq = seq, f_head, f_chunk, f_ctx = context(seq), f_off;
-  [[maybe_unused]] int own_left = 0;  // team: further chunks of a short item of this warp's
   const int32_t* f_entry;          // of the group in the block table
   const int step_idx = CT / bs, step_off = CT - step_idx * bs;
   auto place = [&]() {
@@ -287,23 +286,20 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
     f_chunk = rel - f_head * n;
     place();
   }
-  // on to the item of the cursor's chunk (which exists), if that is a later one
-  auto settle = [&]() {
-    if (f_chunk * CT < f_ctx) return false;
-    do {
-      f_chunk -= (f_ctx + CT - 1) / CT;
-      if (++f_head == Hkv) {
-        f_head = 0;
-        do {
-          f_ctx = context(++f_seq);
-        } while (f_ctx == 0);
-      }
-    } while (f_chunk * CT >= f_ctx);
-    place();
-    // its queries will be wanted in a moment
+  // on to the first chunk of the next item, which exists
+  auto next_item = [&]() {
+    f_chunk = 0;
+    if (++f_head == Hkv) {
+      f_head = 0;
+      do {
+        f_ctx = context(++f_seq);
+      } while (f_ctx == 0);
+    }
+  };
+  // the cursor's item's queries will be wanted in a moment
+  auto warm = [&]() {
     const char* q = reinterpret_cast<const char*>(a.q + ((size_t)f_seq * a.num_q_heads + f_head * G) * D);
     if (lane * 128 < G * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
-    return true;
   };
   struct Group {
     int chunk, blk, off, head;  // chunk (the span's end: none), table entry, first token in the block (negative:
@@ -311,29 +307,20 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   };
   auto fetch = [&]() {
     Group e{span_end, 0, -1, 0};
-    if constexpr (TEAM) {
-      int c = f_at + 1;  // of a short item of this warp's
-      if (own_left > 0) --own_left;
-      else own_left = -1;
+    if constexpr (TEAM) {  // from the cursor on, this warp's next chunk
+      bool moved = false;
       for (;;) {
-        if (own_left < 0) {
-          if (lane == 0) c = atomicAdd(claims, 1);
-          c = __shfl_sync(0xffffffffu, c, 0);
-          if (c >= span_end) {
-            own_left = 0;
-            return e;
-          }
-        }
-        f_chunk += c - f_at;
-        f_at = c;
-        if (!settle()) place();
-        if (own_left >= 0) break;
-        const int n = (f_ctx + CT - 1) / CT, start = c - f_chunk;
-        const bool solo = n <= kFp4Solo && start >= span_begin && start + n <= span_end;
-        if (solo && f_chunk > 0) continue;  // its first chunk's claimer has the whole item
-        own_left = solo ? n - 1 : 0;
-        break;
+        const int n = (f_ctx + CT - 1) / CT, start = f_at - f_chunk;
+        if (!one_warps(start, n)) f_chunk += (warp - (f_at - span_begin)) & (NW - 1);
+        else if (owner(f_seq, f_head) != warp) f_chunk = n;
+        f_at = start + min(f_chunk, n);
+        if (f_at >= span_end) return e;
+        if (f_chunk < n) break;
+        next_item();
+        moved = true;
       }
+      place();
+      if (moved) warm();
     }
     if (TEAM || f_at < span_end) {
       e.chunk = f_at;
@@ -342,12 +329,17 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
         e.off = f_off;
         e.blk = __ldg(f_entry);
       }
-      if (!TEAM && ++f_at < span_end) {
-        ++f_chunk;
+      ++f_at;
+      ++f_chunk;
+      if (!TEAM && f_at < span_end) {
         f_entry += step_idx;
         f_off += step_off;
         if (f_off >= bs) { f_off -= bs; ++f_entry; }
-        settle();
+        if (f_chunk * CT >= f_ctx) {
+          next_item();
+          place();
+          warm();
+        }
       }
     }
     return e;
@@ -396,9 +388,8 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   Group next = fetch();
   for (;;) {
     const int item_chunks = (ctx + CT - 1) / CT, len = min(item_chunks - first, span_end - at);
-    // a team leaves short whole items to the warp that has claimed them
-    const bool solo = TEAM && first == 0 && len == item_chunks && item_chunks <= kFp4Solo;
-    if (!solo || (next.chunk >= at && next.chunk < at + len)) {
+    const bool solo = one_warps(at - first, item_chunks);
+    if (!solo || owner(seq, kvh) == warp) {
       // what may be copied by now: a team's stages are free for its merge at the item's end
       const int copy_end = TEAM ? at + len : span_end;
       while (issued - k < NST && next.chunk < copy_end) {
@@ -867,11 +858,11 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
               if (last) __stcg(word, 0ull);  // for a replay of the same call
               // Orders the count before the reads below: here, then for the other threads by the barrier (a shuffle orders nothing).
               __threadfence();
-              if constexpr (TEAM) claims[1] = last;
+              if constexpr (TEAM) *reinterpret_cast<volatile int*>(smem + L::kTeam) = last;
             }
             if constexpr (TEAM) {
               __syncthreads();
-              last = *reinterpret_cast<volatile int*>(claims + 1) != 0;
+              last = *reinterpret_cast<volatile int*>(smem + L::kTeam) != 0;
             } else {
               last = __shfl_sync(0xffffffffu, (int)last, 0);
               __syncwarp();

@@ -58,3 +58,16 @@ def test_merges_repeat(dtype, group, d):
     rng = np.random.default_rng(group + d + dtype)
     c = ref.quantised_case(rng, dtype=dtype, hq=2 * group, hkv=2, d=d, bs=16, ctx=[130, 700, 1600, 5000, 12000])
     _repeat(c, dtype, 40)
+
+
+@pytest.mark.parametrize("dtype", [gen.F16, gen.BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("ctx", [[20000], [8000, 7000, 50, 300, 0, 8192], [64, 5, 0, 2000, 63, 65, 192, 256, 257, 320, 9, 8000],
+                                 [130, 250, 40, 1, 200, 100, 64, 12, 31] * 4 + [3000]],
+                         ids=["one", "long", "ragged", "short"])
+@pytest.mark.parametrize("bs", [8, 16, 64])
+def test_teams_repeat(dtype, ctx, bs):
+    """16 heads of 64 and fewer items than CTAs: a CTA's warps share a span, and which of them adds what up must not
+    follow from whose copies land first."""
+    rng = np.random.default_rng(len(ctx) + bs)
+    c = ref.quantised_case(rng, dtype=dtype, hq=32, hkv=2, d=64, bs=bs, ctx=ctx)
+    _repeat(c, dtype, 60)
