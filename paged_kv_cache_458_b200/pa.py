@@ -172,7 +172,9 @@ def _ptr(x) -> int | None:
     try:
         return x.data_ptr()
     except AttributeError:
-        return x  # an address
+        if not isinstance(x, int):  # an address; anything else is a mistake
+            raise
+        return x
 
 
 _current_stream = None
