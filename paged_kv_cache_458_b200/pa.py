@@ -188,8 +188,11 @@ def _stream(stream) -> int | None:
 
             torch.cuda.current_stream()  # initialises CUDA
             # the handle without a Stream object around it: 0.2 us instead of 3.2 us a call
-            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-            _current_stream = lambda: raw(device())  # noqa: E731
+            raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            if raw and device:
+                _current_stream = lambda: raw(device())  # noqa: E731
+            else:
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
         return _current_stream()
     if isinstance(stream, int):
         return stream

@@ -20,3 +20,20 @@ def test_tensors_addresses_and_none_pass():
     torch = pytest.importorskip("torch")
     t = torch.zeros(4)
     assert pa._ptr(t) == t.data_ptr() and pa._ptr(4096) == 4096 and pa._ptr(None) is None
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_current_stream_with_and_without_the_fast_query(monkeypatch, fast):
+    """Without a stream the call goes to torch's current one, also where torch lacks the calls that ask for its handle."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(pa, "_current_stream", None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: type("Stream", (), {"cuda_stream": 77})())
+    if fast:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 + device, raising=False)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+        monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    for _ in range(2):
+        assert pa._stream(None) == (1003 if fast else 77)
+    assert pa._stream(5) == 5
