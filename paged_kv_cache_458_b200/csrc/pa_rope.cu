@@ -112,9 +112,9 @@ __device__ __forceinline__ uint2 e4m3x8_of(const uint32_t (&w)[4], const HeadSca
     f[2 * j] = v.x;
     f[2 * j + 1] = v.y;
   }
-  // a quotient beyond fp32 (a bf16 row) must come out infinite, not NaN; fp16's are below 2^77
+  // a quotient beyond fp32 (a bf16 row) must come out infinite, not NaN, also beside a NaN; fp16's are below 2^77
   bool safe = s.safe;
-  if (!std::is_same<T, __half>::value) safe = safe && !(magnitude<T>(top8<T>(w)) * s.y >= 0x1p100f);
+  if (!std::is_same<T, __half>::value) safe = safe && magnitude<T>(top8<T>(w)) * s.y < 0x1p100f;
   if (safe) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = div_by(f[j], s.h, s.y);
