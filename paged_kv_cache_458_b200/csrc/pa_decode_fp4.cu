@@ -51,13 +51,11 @@
 //   K: thread (g, t) = (lane / 4, lane % 4) holds dims [t D/4, (t + 1) D/4) of
 //      the tile's tokens perm(g) and perm(g) + 8;
 //   V: thread (g, t) holds dims [g D/8, (g + 1) D/8) of tokens t, t + 4, t + 8, t + 12;
-//      A register holds two neighbours of the contraction.  Up to groups of 8
-//      these are the two dims of a byte: the contraction runs over (token,
-//      parity of the dim), against a column that holds p for one parity and 0 for
-//      the other, so the output's columns are (head, parity): 8 of them for 4 heads,
-//      16 for 8.  For 16 heads that would take 32 columns and twice the matrix
-//      instructions, which bound that case; there nibbles of two tokens are paired
-//      into bytes (one shift and one 3-input logic op per four) before widening.
+//      A register holds two neighbours of the contraction, two tokens here: nibbles of
+//      both are paired into bytes (one shift and one 3-input logic op per four) before
+//      widening.  (Pairing the two dims of a byte instead, against a column that holds p for
+//      one and 0 for the other, needs no such step, but a column per head and parity: with p in
+//      two parts (below) 96.1 us against 94.4 at 4 heads, 150 against 132 at 8.)
 // The 8 x 8 transposes from S^T's layout to P^T's are one movmatrix each.
 //
 // Softmax per warp in the log2 domain.  The reference m of a head lies 7 below a
@@ -68,9 +66,11 @@
 //
 // Roundings: q is bf16 or f16; a bf16 row is scaled by a power of two to a
 // largest magnitude in [2^14, 2^15) and is then exact in f16 down to 2^-29 of it.
-// p enters the second product as one f16 for bf16 outputs (2^-11 relative, against
-// the output's 2^-8) and as hi + lo, 22 bits, for f16 outputs.  Sums, the
-// softmax statistics and the partial results are fp32.
+// p enters the second product as hi + lo, two f16 of 22 bits together, so that the product
+// keeps what the sums keep: as one f16 p is 2^-12 off, which shows where V's cancel.  Up to
+// groups of 4 the columns 4 .. 7 of a tile repeat the heads and take the lo parts; beyond, lo is a
+// product of its own (one f16 against two: 128 sequences, 32/8 heads 88 us and 94; 6 long ones,
+// 64/8 heads 126 and 132).  Sums, the softmax statistics and the partial results are fp32.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -110,9 +110,10 @@ struct Fp4Smem {
 template <int D, int GT>
 struct Fp4State {
   static constexpr int NS = GT == 16 ? 2 : 1;            // tiles of 8 columns of logits
-  static constexpr int NV = GT == 4 ? 1 : 2;             // of outputs: with pairs of dims a column per head and parity
-  static constexpr int MT = GT == 16 ? D / 16 : D / 32;  // 16-row tiles of output dims, or of pairs of dims
-  static constexpr int kBytes = (MT * NV + NS) * 32 * 16;
+  static constexpr bool kFolded = GT == 4;               // columns 0 .. 3 hold the heads' hi parts, 4 .. 7 their lo parts
+  static constexpr int MT = D / 16;                      // 16-row tiles of output dims
+  static constexpr int MS = kFolded ? MT / 2 : MT;       // as stored: hi and lo added up, each thread keeps half of the rows
+  static constexpr int kBytes = (MS + 1) * NS * 32 * 16;
 };
 int fp4_state_bytes(int head_dim, int group) {
   if (head_dim == 128) return group <= 4 ? Fp4State<128, 4>::kBytes : group <= 8 ? Fp4State<128, 8>::kBytes : Fp4State<128, 16>::kBytes;
@@ -167,11 +168,9 @@ __global__ void __launch_bounds__(kFp4Warps * 32, fp4_ctas(D, GT))
 decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
                   const unsigned char* __restrict__ v_pool, const int num_workers, float4* partials,
                   unsigned long long* arrivals) {
-  constexpr int NS = Fp4State<D, GT>::NS, NV = Fp4State<D, GT>::NV, MT = Fp4State<D, GT>::MT;
-  constexpr bool kPairs = GT <= 8;  // V registers hold pairs of dims (see above), else pairs of tokens
-  constexpr bool kFolded = GT == 4;  // both dims of a pair in one column tile: even ones in columns 0 .. 3, odd in 4 .. 7
+  constexpr int NS = Fp4State<D, GT>::NS, MT = Fp4State<D, GT>::MT, MS = Fp4State<D, GT>::MS;
+  constexpr bool kFolded = Fp4State<D, GT>::kFolded;
   using L = Fp4Smem<D>;
-  constexpr bool kLo = std::is_same<T, __half>::value;  // p as hi + lo
   constexpr int NW = kFp4Warps, NST = kFp4Stages, CT = kFp4Chunk, TILES = 2;
   constexpr int KW = D / 32;   // words of K codes a thread takes per row
   constexpr int VW = D / 64;   // words of V codes a thread takes per row
@@ -375,9 +374,6 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
   const int k_row = (g >> 1) + 4 * (g & 1);  // token of the tile's row g (row g + 8: 8 tokens on)
   const int k_code = k_row * (D / 2) + t * (D / 8);
   const int k_sc = kScaleBase + k_row * (D / 16) + t * (D / 64);
-  // pairs: where a transposed probability of token t (or t + 4) goes: the even dim's
-  // place in columns 0 .. 3, the odd dim's in columns 4 .. 7
-  [[maybe_unused]] const uint32_t pair_lo = g < 4 ? 0x4410 : 0x1044, pair_hi = g < 4 ? 0x4432 : 0x3244;
   const int v_code = L::kPoolBytes + t * (D / 2) + g * (D / 16);
   const int v_sc = L::kPoolBytes + kScaleBase + t * (D / 16) + g * (D / 64) / 2;
 
@@ -415,7 +411,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
           w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         }
         float down = 1.f;
-        if constexpr (!kLo) {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
           float top = 0.f;
 #pragma unroll
           for (int i = 0; i < KW * 4; ++i) {
@@ -441,14 +437,13 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
         xs[n][1] = __shfl_sync(0xffffffffu, pos, 8 * t + 4);
       }
 
-      float o[MT][NV][4], m[NS][2], l[NS][2];
-      constexpr auto tile_of = [](int v) { return GT == 16 ? v : 0; };  // the logits' tile of an output tile
+      float o[MT][NS][4], m[NS][2], l[NS][2];
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+      for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[i][v][j] = 0.f;
+          for (int j = 0; j < 4; ++j) o[i][n][j] = 0.f;
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         m[n][0] = m[n][1] = kFp4Lowest;
@@ -562,14 +557,10 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
                 m[n][j] = mn;
                 l[n][j] *= al;
 #pragma unroll
-                for (int w = 0; w < NV; ++w)
-                  if (tile_of(w) == n) {
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                      o[i][w][j] *= al;
-                      o[i][w][j + 2] *= al;
-                    }
-                  }
+                for (int i = 0; i < MT; ++i) {
+                  o[i][n][j] *= al;
+                  o[i][n][j + 2] *= al;
+                }
               }
           }
 
@@ -586,11 +577,10 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
                 l[n][0] += p0;
                 l[n][1] += p1;
                 const uint32_t h = f16x2_of(p0, p1);
-                hi[n][j] = transpose_8x8(h);
-                if constexpr (kLo) {
-                  const float2 f = h2_to_f2(h);
-                  lo[n][j] = transpose_8x8(f16x2_of(p0 - f.x, p1 - f.y));
-                }
+                const float2 f = h2_to_f2(h);
+                const uint32_t r = f16x2_of(p0 - f.x, p1 - f.y);
+                hi[n][j] = transpose_8x8(kFolded && t >= 2 ? r : h);
+                if constexpr (!kFolded) lo[n][j] = transpose_8x8(r);
               }
             const unsigned char* va = st + v_code + i * kCodeTile;
             const unsigned char* vs = st + v_sc + i * kScaleTile;
@@ -608,65 +598,28 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 #pragma unroll
             for (int r = 0; r < 2; ++r)
               sc[r] = e4m3x2_to_h2((uint16_t)(vs[r * kScaleHalf] | (vs[4 * (D / 16) + r * kScaleHalf] << 8)));
-            if constexpr (kPairs) {
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {  // 8 tokens a product: t and t + 4, then t + 8 and t + 12
-                const uint32_t s0 = __byte_perm(sc[r], 0, 0x1010), s1 = __byte_perm(sc[r], 0, 0x3232);
-                uint32_t b0[NV], b1[NV], d0[NV], d1[NV];
+            for (int w = 0; w < VW; ++w) {
+              uint32_t ev[2][4], od[2][4];  // [token pair][j]: dims 2j and 2j + 1 of the word
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                  const uint32_t at_lo = kFolded ? pair_lo : v ? 0x1044 : 0x4410, at_hi = kFolded ? pair_hi : v ? 0x3244 : 0x4432;
-                  b0[v] = __byte_perm(hi[0][r], 0, at_lo);
-                  b1[v] = __byte_perm(hi[0][r], 0, at_hi);
-                  if constexpr (kLo) {
-                    d0[v] = __byte_perm(lo[0][r], 0, at_lo);
-                    d1[v] = __byte_perm(lo[0][r], 0, at_hi);
-                  }
-                }
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t u0 = c[2 * r][w], u1 = c[2 * r + 1][w];
+                e2m1x8_to_h2((u0 & 0x0f0f0f0fu) | ((u1 << 4) & 0xf0f0f0f0u), ev[r]);
+                e2m1x8_to_h2(((u0 >> 4) & 0x0f0f0f0fu) | (u1 & 0xf0f0f0f0u), od[r]);
 #pragma unroll
-                for (int w = 0; w < VW; ++w) {
-                  uint32_t f0[4], f1[4];
-                  e2m1x8_to_h2(c[2 * r][w], f0);
-                  e2m1x8_to_h2(c[2 * r + 1][w], f1);
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    f0[j] = hmul2(f0[j], s0);
-                    f1[j] = hmul2(f1[j], s1);
-                  }
-#pragma unroll
-                  for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                      mma_f16(o[2 * w + j][v], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], b0[v], b1[v]);
-                      if constexpr (kLo)
-                        mma_f16(o[2 * w + j][v], f0[2 * j], f0[2 * j + 1], f1[2 * j], f1[2 * j + 1], d0[v], d1[v]);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                  ev[r][j] = hmul2(ev[r][j], sc[r]);
+                  od[r][j] = hmul2(od[r][j], sc[r]);
                 }
               }
-            } else {
 #pragma unroll
-              for (int w = 0; w < VW; ++w) {
-                uint32_t ev[2][4], od[2][4];  // [token pair][j]: dims 2j and 2j + 1 of the word
+              for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  const uint32_t u0 = c[2 * r][w], u1 = c[2 * r + 1][w];
-                  e2m1x8_to_h2((u0 & 0x0f0f0f0fu) | ((u1 << 4) & 0xf0f0f0f0u), ev[r]);
-                  e2m1x8_to_h2(((u0 >> 4) & 0x0f0f0f0fu) | (u1 & 0xf0f0f0f0u), od[r]);
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    ev[r][j] = hmul2(ev[r][j], sc[r]);
-                    od[r][j] = hmul2(od[r][j], sc[r]);
-                  }
+                for (int n = 0; n < NS; ++n) {
+                  mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], hi[n][0], hi[n][1]);
+                  if constexpr (!kFolded)
+                    mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], lo[n][0], lo[n][1]);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int n = 0; n < NS; ++n) {
-                    mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], hi[n][0], hi[n][1]);
-                    if constexpr (kLo)
-                      mma_f16(o[4 * w + j][n], ev[0][j], od[0][j], ev[1][j], od[1][j], lo[n][0], lo[n][1]);
-                  }
-              }
             }
           }
         }
@@ -688,38 +641,18 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
           if (failed) l[n][j] = __int_as_float(0x7fc00000);
         }
 
-      // Writes the outputs of a row of the state: x[v] are its tiles, f the columns' factors.
-      auto emit = [&](int row, const float4 (&x)[NV], const float (&f)[NS][2]) {
+      // Writes row `row` of the state's outputs: x[n] are its tiles, f the columns' factors.
+      auto emit = [&](int row, const float4 (&x)[NS], const float (&f)[NS][2]) {
         auto pair = [](float v0, float v1) {
           return (uint32_t)Elem<T>::from_f(v0) | ((uint32_t)Elem<T>::from_f(v1) << 16);
         };
-        uint16_t* out = a.out + head0 * D + g * (D / 8);  // this thread's dims of head 0
+        // this thread's dims of head 0: from the tile's rows g and g + 8
+        uint16_t* out = a.out + head0 * D + g * (D / 8) + 2 * (kFolded && t >= 2 ? row + MS : row);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {  // columns 2t and 2t + 1
-          auto first_of = [&](int v) { return j ? x[v].y : x[v].x; };   // of the tile's row g
-          auto second_of = [&](int v) { return j ? x[v].w : x[v].z; };  // of row g + 8
-          if constexpr (kFolded) {
-            // threads t < 2 hold the even dims of two pairs, t >= 2 the odd ones: each takes one pair
-            float v0 = first_of(0) * f[0][j], v1 = second_of(0) * f[0][j];
-            const float got = __shfl_xor_sync(0xffffffffu, t < 2 ? v1 : v0, 2);
-            if (t < 2) v1 = got;
-            else v0 = got;
-            const int h = 2 * (t & 1) + j;
-            if (h < G) *reinterpret_cast<uint32_t*>(out + h * D + 4 * row + 2 * (t >> 1)) = pair(v0, v1);
-          } else if constexpr (kPairs) {
-            const int h = 2 * t + j;
-            if (h < G)
-              *reinterpret_cast<uint2*>(out + h * D + 4 * row) =
-                  make_uint2(pair(first_of(0) * f[0][j], first_of(1) * f[0][j]),
-                             pair(second_of(0) * f[0][j], second_of(1) * f[0][j]));
-          } else {
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              const float fv = f[tile_of(v)][j];
-              const int h = v * 8 + 2 * t + j;
-              if (h < G) *reinterpret_cast<uint32_t*>(out + h * D + 2 * row) = pair(first_of(v) * fv, second_of(v) * fv);
-            }
-          }
+        for (int n = 0; n < NS; ++n) {
+          const int h = n * 8 + (kFolded ? 2 * (t & 1) : 2 * t);  // and h + 1
+          if (h < G) *reinterpret_cast<uint32_t*>(out + h * D) = pair(x[n].x * f[n][0], x[n].z * f[n][0]);
+          if (h + 1 < G) *reinterpret_cast<uint32_t*>(out + (h + 1) * D) = pair(x[n].y * f[n][1], x[n].w * f[n][1]);
         }
       };
       auto factors = [&](float (&f)[NS][2]) {
@@ -735,21 +668,21 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
         factors(f);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          float4 y[NV];
+          float4 y[NS];
 #pragma unroll
-          for (int v = 0; v < NV; ++v) y[v] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
+          for (int n = 0; n < NS; ++n) y[n] = make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
           emit(i, y, f);
         }
       } else {
 
         // From here a warp holds the rows i = row0, row0 + rows_step, ... of the
-        // state o[i][v] (all of them, or a team's warp every fourth) and every m and l.
+        // stored state (all of them, or a team's warp every fourth) and every m and l.
         const int row0 = TEAM ? warp : 0;
-        constexpr int rows_step = TEAM ? NW : 1, ROWS = (MT + rows_step - 1) / rows_step;
-        float4 x[ROWS][NV];
-        auto has = [&](int i) { return !TEAM || row0 + i * rows_step < MT; };
-        auto at_row = [&](int i, int v) { return (v * MT + row0 + i * rows_step) * 32; };  // in a stored state
-        auto at_ml = [&](int n) { return (MT * NV + n) * 32; };
+        constexpr int rows_step = TEAM ? NW : 1, ROWS = (MS + rows_step - 1) / rows_step;
+        float4 x[ROWS][NS];
+        auto has = [&](int i) { return !TEAM || row0 + i * rows_step < MS; };
+        auto at_row = [&](int i, int n) { return (n * MS + row0 + i * rows_step) * 32; };  // in a stored state
+        auto at_ml = [&](int n) { return (MS * NS + n) * 32; };
         // adds w0, w1 (columns 2t, 2t + 1) times a stored state's rows
         auto add = [](float4& to, const float4& v, float w0, float w1) {
           to.x = fmaf(v.x, w0, to.x);
@@ -760,9 +693,9 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
         if constexpr (TEAM) {
           float4* state = reinterpret_cast<float4*>(stages) + lane;  // every warp's, in its own stages
 #pragma unroll
-          for (int v = 0; v < NV; ++v)
+          for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) state[(v * MT + i) * 32] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
+            for (int i = 0; i < MT; ++i) state[(n * MT + i) * 32] = make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
 #pragma unroll
           for (int n = 0; n < NS; ++n) state[at_ml(n)] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
           __syncthreads();
@@ -792,17 +725,28 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 #pragma unroll
           for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              x[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int n = 0; n < NS; ++n) {
+              x[i][n] = make_float4(0.f, 0.f, 0.f, 0.f);
               if (!has(i)) continue;
 #pragma unroll
-              for (int w = 0; w < NW; ++w) add(x[i][v], of[w][at_row(i, v)], w0[tile_of(v)][w], w1[tile_of(v)][w]);
+              for (int w = 0; w < NW; ++w) add(x[i][n], of[w][at_row(i, n)], w0[n][w], w1[n][w]);
             }
         } else {
 #pragma unroll
-          for (int v = 0; v < NV; ++v)
+          for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) x[i][v] = make_float4(o[i][v][0], o[i][v][1], o[i][v][2], o[i][v][3]);
+            for (int i = 0; i < ROWS; ++i) {
+              float y[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y[j] = o[i][n][j];
+                if constexpr (kFolded) {  // threads t < 2 keep the first half of the rows, t >= 2 the second
+                  const float other = __shfl_xor_sync(0xffffffffu, t < 2 ? o[i + MS][n][j] : y[j], 2);
+                  y[j] = (t < 2 ? y[j] : o[i + MS][n][j]) + other;
+                }
+              }
+              x[i][n] = make_float4(y[0], y[1], y[2], y[3]);
+            }
         }
 
         // ---- an item cut by span borders: merge what has arrived
@@ -820,10 +764,10 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
           for (;;) {
             float4* mine = slot(node);
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
+            for (int n = 0; n < NS; ++n)
 #pragma unroll
               for (int i = 0; i < ROWS; ++i)
-                if (has(i)) __stcg(mine + at_row(i, v), x[i][v]);
+                if (has(i)) __stcg(mine + at_row(i, n), x[i][n]);
             if (row0 == 0) {
 #pragma unroll
               for (int n = 0; n < NS; ++n) __stcg(mine + at_ml(n), make_float4(m[n][0], m[n][1], l[n][0], l[n][1]));
@@ -871,7 +815,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
             // all children, in order, kBatch of them in flight
             constexpr int kBatch = TEAM ? 4 : GT == 4 ? 4 : GT == 8 ? 2 : 1;
             for (int c0 = 0; c0 < kids; c0 += kBatch) {
-              float4 y[kBatch][ROWS][NV], ml[kBatch][NS];
+              float4 y[kBatch][ROWS][NS], ml[kBatch][NS];
 #pragma unroll
               for (int b = 0; b < kBatch; ++b) {
                 const float4* from = slot(up + min(c0 + b, kids - 1) * width);
@@ -880,8 +824,8 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 #pragma unroll
                 for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-                  for (int v = 0; v < NV; ++v)
-                    if (has(i)) y[b][i][v] = __ldcg(from + at_row(i, v));
+                  for (int n = 0; n < NS; ++n)
+                    if (has(i)) y[b][i][n] = __ldcg(from + at_row(i, n));
               }
               float a0[NS], a1[NS];  // weights of what has been added up so far
 #pragma unroll
@@ -902,9 +846,9 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 #pragma unroll
               for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                  const float w0 = a0[tile_of(v)], w1 = a1[tile_of(v)];
-                  x[i][v] = c0 ? make_float4(x[i][v].x * w0, x[i][v].y * w1, x[i][v].z * w0, x[i][v].w * w1)
+                for (int n = 0; n < NS; ++n) {
+                  const float w0 = a0[n], w1 = a1[n];
+                  x[i][n] = c0 ? make_float4(x[i][n].x * w0, x[i][n].y * w1, x[i][n].z * w0, x[i][n].w * w1)
                                : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
@@ -921,8 +865,8 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
 #pragma unroll
                   for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-                    for (int v = 0; v < NV; ++v)
-                      if (has(i)) add(x[i][v], y[b][i][v], w0[tile_of(v)], w1[tile_of(v)]);
+                    for (int n = 0; n < NS; ++n)
+                      if (has(i)) add(x[i][n], y[b][i][n], w0[n], w1[n]);
                 }
             }
             node = up;
