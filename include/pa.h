@@ -388,7 +388,8 @@ pa_status pa_cache_append_fp4(const void *k, const void *v, const int32_t *slot_
  * shared_prefix, blocks of less than 2^31 bytes, num_seqs and max_context_len up to
  * 2^30 (else PA_ERR_UNSUPPORTED).  The batch's tokens are split evenly over the
  * device whatever the contexts; partition_tokens is the least a warp takes (0:
- * 64), and only bounds the split of small batches.  workspace: at least
+ * 64) as long as the contexts hold that much, whatever max_context_len says, and only
+ * bounds the split of small batches.  workspace: at least
  * pa_decode_workspace_bytes(shape, max_context_len) bytes, with this call's
  * shape and max_context_len; any contents; not shared with a decode that runs
  * concurrently.  The same inputs give the same bits whatever the timing.

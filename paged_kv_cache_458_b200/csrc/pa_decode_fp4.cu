@@ -166,7 +166,7 @@ __device__ __forceinline__ float ex2(float x) {
 template <typename T, int D, int GT, int R, bool TEAM>
 __global__ void __launch_bounds__(kFp4Warps * 32, fp4_ctas(D, GT))
 decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
-                  const unsigned char* __restrict__ v_pool, const int num_workers, float4* partials,
+                  const unsigned char* __restrict__ v_pool, const int num_workers, const int least, float4* partials,
                   unsigned long long* arrivals) {
   constexpr int NS = Fp4State<D, GT>::NS, MT = Fp4State<D, GT>::MT, MS = Fp4State<D, GT>::MS;
   constexpr bool kFolded = Fp4State<D, GT>::kFolded;
@@ -220,14 +220,14 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
     if (lane >= d) run_end += v;
   }
   const int chunks = __shfl_sync(0xffffffffu, run_end, 31);  // below 2^31
-  const int workers = min(num_workers, chunks);  // so that no span among them is empty
+  const int workers = max(1, min(num_workers, chunks / least));  // spans of `least` chunks or more, where there are as many
   // sequences without tokens: zero rows
   for (int s = blockIdx.x + gridDim.x * warp; s < S; s += gridDim.x * NW)
     if (context(s) == 0) {
       uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)s * a.num_q_heads * D);
       for (int i = lane; i < a.num_q_heads * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
     }
-  if (worker >= workers) return;
+  if (worker >= workers || chunks == 0) return;
   const int span_begin = (int)((long long)chunks * worker / workers);
   const int span_end = (int)((long long)chunks * (worker + 1) / workers);
   // opens this span's arrival word: no count of another call is above the tag, and one of this call's stays
@@ -920,7 +920,7 @@ cudaError_t launch_fp4(const DecodeArgs& a, const Fp4Launch& w) {
   const cudaError_t e = allow_smem(kern, Fp4Smem<D>::kTotal, &configured);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(w.split.ctas), dim3(kFp4Warps * 32), Fp4Smem<D>::kTotal, w.stream, a, w.k, w.v,
-                    w.split.workers, w.partials, w.arrivals);
+                    w.split.workers, w.split.least, w.partials, w.arrivals);
 }
 
 template <typename T, int D, int GT, int R>
@@ -954,7 +954,7 @@ cudaError_t launch_fp4_dim(const DecodeArgs& a, int head_dim, const Fp4Launch& w
 
 bool fp4_decode_split(int num_seqs, int num_kv_heads, int group, int head_dim, int max_context_len, int partition_tokens,
                       Fp4Split* w) {
-  *w = Fp4Split{1, 1, false};
+  *w = Fp4Split{1, 1, 1, false};
   if (num_seqs == 0) return true;
   if (num_seqs > 1 << 30 || max_context_len > 1 << 30) return false;  // sums with a chunk or a scan's step stay in 31 bits
   const long long per_item = (max_context_len + kFp4Chunk - 1) / kFp4Chunk, items = (long long)num_seqs * num_kv_heads;
@@ -962,8 +962,8 @@ bool fp4_decode_split(int num_seqs, int num_kv_heads, int group, int head_dim, i
   const int wave = 148 * fp4_ctas(head_dim, group);  // CTAs that a B200 holds at once
   w->team = head_dim == 64 && group > 8 && items < wave;  // see the top of this file
   // a warp takes a chunk at least, or the caller's partition
-  const int least = (partition_tokens > 0 ? (partition_tokens + kFp4Chunk - 1) / kFp4Chunk : 1) * (w->team ? kFp4Warps : 1);
-  const long long most = (per_item * items + least - 1) / least, all = w->team ? wave : wave * kFp4Warps;
+  w->least = (partition_tokens > 0 ? (partition_tokens + kFp4Chunk - 1) / kFp4Chunk : 1) * (w->team ? kFp4Warps : 1);
+  const long long most = per_item * items / w->least, all = w->team ? wave : wave * kFp4Warps;
   w->workers = (int)(most < 1 ? 1 : most < all ? most : all);
   w->ctas = w->workers < wave ? w->workers : wave;
   return true;

@@ -173,10 +173,11 @@ cudaError_t launch_cache_gather(const GatherArgs& a, int dtype, int head_dim, in
                                 cudaStream_t stream, int* launches);
 
 // Attention over an E2M1 cache (pa_decode_fp4.cu): how a batch is split (false:
-// too many chunks).  `partials` holds 2 * workers states of fp4_state_bytes,
+// too many chunks): at most `workers`, each with `least` chunks where the
+// contexts have them.  `partials` holds 2 * workers states of fp4_state_bytes,
 // `arrivals` a word per worker (any contents: counts carry a.epoch as their tag).
 struct Fp4Split {
-  int ctas, workers;
+  int ctas, workers, least;
   bool team;  // a worker is a CTA (else a warp)
 };
 bool fp4_decode_split(int num_seqs, int num_kv_heads, int group, int head_dim, int max_context_len, int partition_tokens,
