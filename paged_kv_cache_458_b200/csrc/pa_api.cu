@@ -835,7 +835,7 @@ pa_status pa_rope_append(const void* q, const void* k, const void* v, const int3
   pa_status st = check_pool_shape(shape);
   if (st != PA_OK) return st;
   if (!rope || num_tokens < 0 || shape->num_q_heads <= 0 || rope->max_position <= 0 ||
-      (rope->interleaved != 0 && rope->interleaved != 1))
+      (rope->interleaved != 0 && rope->interleaved != 1) || rope->reserved != 0)
     return PA_ERR_INVALID_ARG;
   if (rope->rotary_dim <= 0 || rope->rotary_dim > shape->head_dim) return PA_ERR_INVALID_ARG;
   if (rope->rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;

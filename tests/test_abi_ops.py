@@ -147,3 +147,9 @@ def test_gather_rejects_bad_arguments(lib, i):
         a[i] = bad
         assert lib.pa_cache_gather(*a, _shape(), None) == INVALID
     assert lib.pa_cache_gather(None, 0, None, None, None, None, None, None, _shape(), None) == OK
+
+
+def test_rope_append_refuses_a_reserved_field_in_use(lib):
+    rope = pa.make_rope(rotary_dim=64, max_position=100)
+    rope.reserved = 1
+    assert _rope(lib, _shape(), rope=ctypes.byref(rope)) == INVALID
