@@ -128,7 +128,6 @@ pa_status check_decode_shape(const pa_shape* s, int32_t max_context_len) {
 }
 
 // Whether pa_decode runs the tensor-core variant for this (valid) shape.
-
 bool tensor_core_kernel(const pa_shape* s, int pt) {
   if (s->variant == PA_DECODE_TENSOR_CORES) return true;
   if (s->variant == PA_DECODE_CUDA_CORES) return false;

@@ -9,7 +9,6 @@
 // code * block scale * head scale (the head scale one fp32 per kv head).
 #pragma once
 
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -17,8 +16,6 @@
 #include "pa_common.cuh"
 
 namespace pa {
-
-constexpr int kFp4Block = 16;  // dims that share a block scale
 
 // Bytes of one (block, kv head) run, and of its codes.
 __host__ __device__ constexpr long long fp4_head_bytes(int block_size, int head_dim) {
@@ -29,8 +26,7 @@ __host__ __device__ constexpr long long fp4_code_bytes(int block_size, int head_
 }
 
 // Eight E2M1 codes (low nibble first) -> eight f16 values, exact.  For words
-// loaded whole: unpacking a zero-extended byte this way gave zeros (nvcc 12.9);
-// e2m1x2_to_f2 takes single bytes.
+// loaded whole: unpacking a zero-extended byte this way gave zeros (nvcc 12.9).
 __device__ __forceinline__ void e2m1x8_to_h2(uint32_t w, uint32_t (&o)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %4;\n\t"
@@ -40,12 +36,6 @@ __device__ __forceinline__ void e2m1x8_to_h2(uint32_t w, uint32_t (&o)[4]) {
       "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
       : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
       : "r"(w));
-}
-
-// Two E2M1 codes (low nibble first) -> two floats, exact.
-__device__ __forceinline__ float2 e2m1x2_to_f2(uint8_t b) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(b), __NV_E2M1);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // Two E4M3 codes (low byte first) -> f16x2, exact.
