@@ -163,8 +163,8 @@ int pa_decode_partition_tokens(const pa_shape *shape);
 /* The kernel pa_decode() runs for `shape`: PA_DECODE_CUDA_CORES or
  * PA_DECODE_TENSOR_CORES (PA_DECODE_AUTO resolved), or
  * PA_DECODE_RESOLVED_SHARED_PREFIX with shape->shared_prefix (a plan kernel,
- * then the tensor-core kernel over every group's row list), or minus the
- * status pa_decode() would refuse the shape with.  Host only; launches
+ * then the tensor-core kernel over every group's row list; PA_DECODE_TENSOR_CORES
+ * for an E2M1 cache, which pa_decode_fp4() reads), or minus the status pa_decode() would refuse the shape with.  Host only; launches
  * nothing. */
 #define PA_DECODE_RESOLVED_SHARED_PREFIX 3
 int pa_decode_resolved_variant(const pa_shape *shape);
@@ -452,8 +452,8 @@ pa_status pa_cache_gather(const int32_t *slot_mapping, int32_t num_tokens, const
 /*
  * Copy-on-write of whole blocks (zingnex.cn section 3.2 item 3): for each
  * pair i, block src_dst_pairs[2i+1] of k_cache and of v_cache becomes a
- * byte copy of block src_dst_pairs[2i] (either cache format: a block is
- * block_size * num_kv_heads * head_dim elements of 2 or 1 bytes).
+ * byte copy of block src_dst_pairs[2i] (any cache format: a block is
+ * block_size * num_kv_heads * head_dim elements of 2, 1 or 9/16 bytes).
  * Destinations must be distinct and no
  * destination may also be a source in the same call.
  * src_dst_pairs: device int32 [num_pairs][2].  num_pairs == 0 launches nothing.
@@ -490,8 +490,7 @@ pa_status pa_last_device_error(pa_stream_t stream, uint32_t *bits_out);
 const char *pa_status_string(pa_status status);
 
 /* Text of the CUDA error behind the calling thread's most recent
- * PA_ERR_CUDA from pa_decode(_fp8), pa_cache_append(_fp8), pa_copy_blocks or
- * pa_last_device_error ("no CUDA error" before the first one).  The string is
+ * PA_ERR_CUDA ("no CUDA error" before the first one).  The string is
  * static; the caller does not free it.  Not part of the method: a diagnostic
  * of this library. */
 const char *pa_last_cuda_error(void);

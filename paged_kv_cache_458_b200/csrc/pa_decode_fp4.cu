@@ -8,13 +8,14 @@
 // where there are fewer items than CTAs, a team: the four warps of a CTA, which take a span's
 // chunks in turn and merge through shared memory at an item's end; whole items
 // of few chunks (kFp4Solo) go to one warp, without a merge.  Which warp takes what is
-// fixed: chunks claimed by whoever came first gave other bits from call to call.  A team cuts an item into a
-// quarter of the parts, and its warps share the merges: 32 sequences of 8000 to 8192 tokens,
-// 64/4 heads of 64, take 42 us against 44.5 by warps, 8 of 50 to 8000 19 against 25.  Elsewhere
-// a team's own merge and its uneven end cost more than they save: 4 sequences of 300 to 40000
-// tokens, 128/8 heads of 128, 63 us by teams and 52 by warps; one of 300 tokens,
-// 32/8 heads, 13.7 and 9.1; 18 of 300 to 16000 63 and 48; 6 of 40000 to
-// 131071 with 64/8 heads 125 and 128; one of 60000 30.5 and 32.4.
+// fixed: chunks claimed by whoever came first gave other bits from call to call.  A team cuts
+// an item into a quarter of the parts, and its warps share the merges: 32 sequences of 8000 to
+// 8192 tokens, 64/4 heads of 64, take 45.6 us against 48.7 by warps, 8 of 50 to 8000 20 against
+// 26, one of 1000 9.7 against 13.9; where all items are short its uneven end costs more (40 of 20
+// to 300 16.2 against 11.2).  At heads of 128 and at smaller groups it costs more than it saves
+// (both sides with p as one f16, see below: 4 sequences of 300 to 40000 tokens, 128/8 heads of
+// 128, 63 us by teams and 52 by warps; one of 300 tokens, 32/8 heads, 13.7 and 9.1; 18 of 300 to
+// 16000 63 and 48; 6 of 40000 to 131071 with 64/8 heads 125 and 128; one of 60000 30.5 and 32.4).
 //
 // Copies.  A warp runs its own ring of two stages of bulk copies, across items: a
 // (block, head) run is contiguous, so a chunk of K is one copy per block (two
@@ -29,12 +30,14 @@
 // 128 sequences: its loads start only when the last span has ended.)
 //
 // What bounds it, on a B200 (128 sequences of 1024 to 4096 tokens, 32/8 heads of
-// 128, bf16; 377 MB, 57.6 us at 6551 GB/s): 87 us, 4.3 TB/s.  Without the
-// arithmetic the same copies take 70 us: 2 us of launch and scan, 61 of streaming at
-// 6.2 TB/s, the rest the first copies' latency and the last warp's lead.  The
-// arithmetic (285 instructions a warp for 16 tokens, 132 of them on the pipe of
-// conversions and logic) then fits between the copies but for some 17 us, 5 of them
-// the merges of cut items.  Measured and not kept: 16 warps per SM with chunks of
+// 128, bf16; 380 MB, 58 us at 6551 GB/s): 94 us, 4.05 TB/s.  It is latency.  No pipe is full:
+// issue slots 56 %, the pipe of conversions and logic 51 %, matrix 22 %, DRAM 47 % (6 long
+// sequences, 64/8 heads: 53, 48, 31 and 42 %), 320 instructions a warp for 16 tokens; 2.7 warps a
+// scheduler do not cover a warp's chain of products, maximum, exponentials, transposes, products.
+// The same copies without the arithmetic take 70 us: 2 us of launch and scan, 61 of streaming at
+// 6.2 TB/s, the rest the first copies' latency and the last warp's lead; of the other 24 us some 5
+// are the merges of cut items.  Measured and not kept (when the whole
+// took 87 us, p being one f16): 16 warps per SM with chunks of
 // 32 tokens (the work per chunk doubles: 98 us), producer warps that issue the
 // copies for twelve others (111 us), one lane issuing all of a warp's copies (93 us),
 // small spans claimed at the end (103 us).
@@ -86,7 +89,7 @@ constexpr int kFp4Warps = 4;
 constexpr int kFp4Chunk = 64;   // tokens a stage holds
 constexpr int kFp4Stages = 2;   // per warp
 // CTAs per SM: 3, by registers and (D = 128) shared memory; 2 where the state of 16 heads of 128 takes 64 registers of a thread,
-// which at 168 spills in the products' loop (128 sequences of 1024 to 4096 tokens, 128/8 heads: 122 us against 197).
+// which at 168 spills in the products' loop (128 sequences of 1024 to 4096 tokens, 128/8 heads: 141 us against 210).
 constexpr int fp4_ctas(int head_dim, int group) { return head_dim == 128 && group > 8 ? 2 : 3; }
 // Children of a merge node, at most: 8; but with a state small enough for four children in flight (GT = 4), all parts of an
 // item of up to 24, so that one level does: a level costs some 2 us, a child 0.15 (16 parts of 64 tokens, 8 heads: 10.5 us
@@ -170,6 +173,7 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
                   unsigned long long* arrivals) {
   constexpr int NS = Fp4State<D, GT>::NS, MT = Fp4State<D, GT>::MT, MS = Fp4State<D, GT>::MS;
   constexpr bool kFolded = Fp4State<D, GT>::kFolded;
+  static_assert(!TEAM || !kFolded, "a team merges states whose hi and lo parts share columns");
   using L = Fp4Smem<D>;
   constexpr int NW = kFp4Warps, NST = kFp4Stages, CT = kFp4Chunk, TILES = 2;
   constexpr int KW = D / 32;   // words of K codes a thread takes per row
