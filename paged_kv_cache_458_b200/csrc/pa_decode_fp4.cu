@@ -400,7 +400,8 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
       const size_t head0 = (size_t)seq * a.num_q_heads + kvh * G;
 
       // queries as column fragments: thread (g, t) holds dims [t D/4, (t + 1) D/4) of heads g, g + 8
-      // The logit scale is kept positive: its sign goes into the queries, and a zero scale zeroes them.
+      // The logit scale is kept positive: its sign goes into the queries, and a zero scale zeroes
+      // them (but for NaN and infinity, which become NaN).
       const float cscale = a.scale_log2 * __ldg(a.k_scale + kvh);
       uint32_t bq[NS][KW * 4];
       float xs[NS][2];  // logit scale of this thread's columns 2t, 2t + 1
@@ -434,8 +435,9 @@ decode_fp4_kernel(const DecodeArgs a, const unsigned char* __restrict__ k_pool,
           }
         }
         const float c = cscale * down;
+        const uint32_t sign = c == 0.f ? 0u : c < 0.f ? 0xbc00bc00u : 0x3c003c00u;  // 0, -1 or 1, twice
 #pragma unroll
-        for (int i = 0; i < KW * 4; ++i) bq[n][i] = c == 0.f ? 0u : c < 0.f ? w[i] ^ 0x80008000u : w[i];
+        for (int i = 0; i < KW * 4; ++i) bq[n][i] = hmul2(w[i], sign);
         const float pos = c == 0.f ? 1.f : fabsf(c);
         xs[n][0] = __shfl_sync(0xffffffffu, pos, 8 * t);
         xs[n][1] = __shfl_sync(0xffffffffu, pos, 8 * t + 4);

@@ -68,3 +68,27 @@ def test_probabilities_keep_more_than_one_f16(dtype, group, d):
     half = {gen.F16: 2.0 ** -11, gen.BF16: 2.0 ** -8}[dtype]
     assert (np.abs(exact) > 1e-3).all() and (np.abs(exact) < 0.2).all()
     assert (np.abs(got - exact) <= np.abs(exact) * half * (1 + 2.0 ** -8) + 6 * 2.0 ** -19).all(), np.abs(got - exact).max()
+
+
+@pytest.mark.parametrize("dtype", [gen.F16, gen.BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, 1e-30, 0.1])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_a_query_that_is_no_number_shows_at_any_scale(dtype, scale, bad):
+    """NaN times a scale of zero is NaN, and so is infinity: not the mean of V.  (An infinite query meets codes of both
+    signs, so its logits are NaN or of both signs at any other scale.)"""
+    rng = np.random.default_rng(1)
+    c = ref.quantised_case(rng, dtype=dtype, hq=8, hkv=2, d=64, bs=16, ctx=[70, 9])
+    q = np.zeros((2, 8, 64), np.float32)
+    q[0, 3, 5] = bad
+    shape = pa.make_shape(num_seqs=2, num_q_heads=8, num_kv_heads=2, head_dim=64, block_size=16, num_blocks=c["num_blocks"],
+                          max_blocks_per_seq=c["block_tables"].shape[1], dtype=dtype, cache_format=pa.PA_CACHE_FP4_E2M1)
+    out = torch.zeros((2, 8, 64), dtype=pa.torch_dtype(dtype), device="cuda")
+    ws = torch.empty(pa.pa_decode_workspace_bytes(shape, 70), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_fp4(dev(gen.to_bits(q, dtype), dtype),
+                     *(torch.from_numpy(c[k]).cuda() for k in ("k_pool", "v_pool", "k_scale", "v_scale")),
+                     dev_i32(c["block_tables"]), dev_i32(c["context_lens"]), scale, out, shape, 70, ws)
+    assert pa.pa_last_device_error()[0] == pa.PA_OK
+    nan = np.isnan(gen.bits_to_f32(host_bits(out), dtype)).all(-1)
+    want = np.zeros((2, 8), bool)
+    want[0, 3] = True
+    assert np.array_equal(nan, want)
